@@ -116,7 +116,10 @@ QZ_API qz_status qz_packed_bytes(int64_t N, int64_t K, int32_t bits, int32_t sym
  * workspace of QZ_OP_QUANTIZE_PACK (per-tensor only) and of the GEMV/GEMM
  * paths that share tiles between CTAs must be zero-filled once before its
  * first use; every call that completes leaves its counters (and the
- * per-tensor word) at zero again, and the rest is scratch.  Host-only.  The kernels
+ * per-tensor word) at zero again, and the rest is scratch.  Where the counters
+ * lie depends on op and sizes (and, for the decode GEMVs, on whether scales
+ * and zeros are 16-byte aligned), so a buffer serves calls that agree in
+ * those; between others it must be zero-filled again.  Host-only.  The kernels
  * size their grids for the device's SM count (a B200 has 148; a device with
  * more is treated as 148); the size returned here serves every SM count up
  * to 148, so it does not depend on the device.

@@ -154,24 +154,29 @@ def _handle(stream):
 
 
 class Workspace:
-    """A zero-filled device workspace that grows on demand.
+    """Zero-filled device workspaces, one per kind and size of call.
 
     Each call leaves the counters in its workspace at zero again (the rest is
-    scratch that every call writes before it reads), so one buffer serves
-    every call issued on one stream.  Calls that may run
-    concurrently need separate Workspace objects.
+    scratch that every call writes before it reads).  Where the counters lie
+    depends on the call's sizes, and another call's scratch may cover them,
+    so calls of different sizes get different buffers: one Workspace serves
+    every call issued on one stream.  Calls that may run concurrently need
+    separate Workspace objects.
     """
 
     def __init__(self, device=None):
         self.device = torch.device(device if device is not None else "cuda")
-        self.buf = None
+        self.bufs = {}
 
-    def get(self, nbytes: int):
+    def get(self, nbytes: int, key=None):
         if nbytes == 0:
             return None
-        if self.buf is None or self.buf.numel() < nbytes:
-            self.buf = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=self.device)
-        return self.buf
+        key = nbytes if key is None else key
+        buf = self.bufs.get(key)
+        if buf is None or buf.numel() < nbytes:
+            buf = self.bufs[key] = torch.zeros(max(nbytes, 256), dtype=torch.uint8,
+                                               device=self.device)
+        return buf
 
     def get_scratch(self, nbytes: int):
         """A second buffer for calls whose workspace is plain scratch (the
@@ -182,8 +187,9 @@ class Workspace:
         return self.scratch
 
 
-def _ws_args(workspace, nbytes, device):
-    """Pointer and size of the call's workspace.  Called inside
+def _ws_args(workspace, nbytes, device, key=None):
+    """Pointer and size of the call's workspace (`key`: what decides where its
+    counters lie, see Workspace).  Called inside
     ``torch.cuda.stream(launch stream)``: a temporary workspace is then
     allocated and zero-filled on the stream the kernel runs on, so the fill
     is ordered before the kernel and the caching allocator hands the memory
@@ -193,7 +199,7 @@ def _ws_args(workspace, nbytes, device):
     if workspace is None:
         workspace = Workspace(device).get(nbytes)
     elif isinstance(workspace, Workspace):
-        workspace = workspace.get(nbytes)
+        workspace = workspace.get(nbytes, key)
     return _ptr(workspace), workspace.numel() * workspace.element_size()
 
 
@@ -247,6 +253,13 @@ def _matmul_out(a, N, y):
     return y
 
 
+def _matmul_key(op, M, N, K, g, scales, zeros):
+    """Workspace key of a split-K call: its sizes, and whether the scale and
+    zero arrays are aligned for the 256-wide plan."""
+    return (op, M, N, K, g, scales.data_ptr() % 16 == 0,
+            zeros is None or zeros.data_ptr() % 16 == 0)
+
+
 def qz_w4a16_gemv(a, codes, scales, zeros, N, K, group_size=128, y=None, workspace=None,
                   stream=None):
     """y = a * w_hat^T for int4 asymmetric group-wise weights, M <= 16."""
@@ -255,7 +268,8 @@ def qz_w4a16_gemv(a, codes, scales, zeros, N, K, group_size=128, y=None, workspa
     with _on(stream):
         y = _matmul_out(a, N, y)
         nbytes = qz_workspace_bytes(QZ_OP_W4A16_GEMV, M, N, K, group_size)
-        ws_ptr, ws_bytes = _ws_args(workspace, nbytes, a.device)
+        ws_ptr, ws_bytes = _ws_args(workspace, nbytes, a.device,
+                                    _matmul_key(QZ_OP_W4A16_GEMV, M, N, K, group_size, scales, zeros))
         _check(lib.qz_w4a16_gemv(_ptr(a), _ptr(codes), _ptr(scales), _ptr(zeros), M, N, K,
                                  group_size, _ptr(y), ws_ptr, ws_bytes, _handle(st)),
                "qz_w4a16_gemv")
@@ -270,7 +284,8 @@ def qz_w4a16_gemm(a, codes, scales, zeros, N, K, group_size=128, y=None, workspa
     with _on(stream):
         y = _matmul_out(a, N, y)
         nbytes = qz_workspace_bytes(QZ_OP_W4A16_GEMM, M, N, K, group_size)
-        ws_ptr, ws_bytes = _ws_args(workspace, nbytes, a.device)
+        ws_ptr, ws_bytes = _ws_args(workspace, nbytes, a.device,
+                                    _matmul_key(QZ_OP_W4A16_GEMM, M, N, K, group_size, scales, zeros))
         _check(lib.qz_w4a16_gemm(_ptr(a), _ptr(codes), _ptr(scales), _ptr(zeros), M, N, K,
                                  group_size, _ptr(y), ws_ptr, ws_bytes, _handle(st)),
                "qz_w4a16_gemm")
@@ -284,7 +299,7 @@ def qz_w8a16_gemv(a, codes, scales, N, K, y=None, workspace=None, stream=None):
     with _on(stream):
         y = _matmul_out(a, N, y)
         nbytes = qz_workspace_bytes(QZ_OP_W8A16_GEMV, M, N, K, K)
-        ws_ptr, ws_bytes = _ws_args(workspace, nbytes, a.device)
+        ws_ptr, ws_bytes = _ws_args(workspace, nbytes, a.device, (QZ_OP_W8A16_GEMV, M, N, K))
         _check(lib.qz_w8a16_gemv(_ptr(a), _ptr(codes), _ptr(scales), M, N, K, _ptr(y),
                                  ws_ptr, ws_bytes, _handle(st)), "qz_w8a16_gemv")
     return y
@@ -297,7 +312,7 @@ def qz_w8a16_gemm(a, codes, scales, N, K, y=None, workspace=None, stream=None):
     with _on(stream):
         y = _matmul_out(a, N, y)
         nbytes = qz_workspace_bytes(QZ_OP_W8A16_GEMM, M, N, K, K)
-        ws_ptr, ws_bytes = _ws_args(workspace, nbytes, a.device)
+        ws_ptr, ws_bytes = _ws_args(workspace, nbytes, a.device, (QZ_OP_W8A16_GEMM, M, N, K))
         _check(lib.qz_w8a16_gemm(_ptr(a), _ptr(codes), _ptr(scales), M, N, K, _ptr(y),
                                  ws_ptr, ws_bytes, _handle(st)), "qz_w8a16_gemm")
     return y
@@ -386,7 +401,8 @@ def qz_fp4a16_gemv(a, codes, scales, tensor_scale, N, K, kind, y=None, workspace
     with _on(stream):
         y = _matmul_out(a, N, y)
         nbytes = qz_workspace_bytes(QZ_OP_FP4A16_GEMV, M, N, K, 0)
-        ws_ptr, ws_bytes = _ws_args(workspace, nbytes, a.device)
+        ws_ptr, ws_bytes = _ws_args(workspace, nbytes, a.device,
+                                    _matmul_key(QZ_OP_FP4A16_GEMV, M, N, K, kind, scales, None))
         _check(lib.qz_fp4a16_gemv(_ptr(a), _ptr(codes), _ptr(scales), _ptr(tensor_scale), M, N,
                                   K, kind, _ptr(y), ws_ptr, ws_bytes, _handle(st)),
                "qz_fp4a16_gemv")
