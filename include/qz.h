@@ -73,7 +73,8 @@ typedef enum {
     QZ_ERR_UNSUPPORTED = 3,     /* a format or shape the kernels do not cover */
     QZ_ERR_WORKSPACE = 4,       /* workspace pointer missing or too small */
     QZ_ERR_CUDA = 5,            /* a CUDA call or launch failed */
-    QZ_ERR_DEVICE_TIMEOUT = 6   /* a bounded device-side wait ran out */
+    QZ_ERR_DEVICE_TIMEOUT = 6,  /* a bounded device-side wait ran out */
+    QZ_ERR_DEVICE_INDEX = 7     /* a page or position read on the device is out of range */
 } qz_status;
 
 /* Operation ids for qz_workspace_bytes. */
@@ -86,7 +87,8 @@ enum {
     QZ_OP_W8A16_GEMM = 5,
     QZ_OP_GPTQ = 6,
     QZ_OP_FP4A16_GEMV = 7,
-    QZ_OP_FP4A4_GEMM = 8
+    QZ_OP_FP4A4_GEMM = 8,
+    QZ_OP_KV4_ATTENTION = 9     /* K = head_dim; M, N (>= 1) and group_size are not used */
 };
 
 /* FP4 formats (kind argument of the qz_fp4_* entry points). */
@@ -366,6 +368,102 @@ QZ_API qz_status qz_fp4a4_gemm(const void *a, const void *codes, const void *sca
                                void *stream);
 
 /*
+ * Paged 4-bit key/value cache.
+ *
+ * Format: the int4 asymmetric group format of qz_quantize_pack, per token,
+ * key head and group of group_size of the head's head_dim values: codes,
+ * scales and zeros are those that qz_quantize_pack gives for a row of
+ * head_dim values, and stand for S (q - Z).
+ * head_dim 64 with group_size 32 or 64; head_dim 128 with 32, 64 or 128;
+ * head_dim 256 with 64 or 128.
+ *
+ * Layout: pages of page_size tokens (a multiple of 16, at most 65536),
+ * [page][kv head][page_size / 16][record]; a record holds 16 tokens of one
+ * head: K codes (8 D bytes), V codes (8 D), K scales [D/g][16] bf16, V scales
+ * [D/g][16] bf16, K zeros [D/g][16] uint8, V zeros [D/g][16] uint8, 16 D +
+ * 96 D/g bytes in all.  With tokens t = 0..15 of the record and word w of
+ * lane l at byte (w / 4 * 32 + l) * 16 + w % 4 * 4 of a code area:
+ *   K: the codes d = 32 j + 8 c + n (nibble n) of token t are word
+ *      t / 8 * (D / 32) + j of lane 4 (t % 8) + c;
+ *   V: the codes d = 64 i + 16 n + 8 e + r (nibble n of a 16-bit half) of
+ *      token t are half t % 2 of word t / 8 * (D / 32) + e * (D / 64) + i of
+ *      lane 4 r + t % 8 / 2.
+ * A cache needs no initial contents.
+ *
+ * Arguments shared by the calls below:
+ *   cache       qz_kv4_cache_bytes bytes, 16-byte aligned
+ *   page_table  int32 [B][max_pages]: page of positions page_size * i ..
+ *               of a sequence; entries behind its length are not read
+ *   kv_lens     int32 [B]: cached tokens of each sequence, the call's own
+ *               tokens included
+ *   cu_tokens   int32 [B + 1], ascending: the call's tokens of sequence b are
+ *               rows cu_tokens[b] .. cu_tokens[b + 1] - 1 of the T rows, and
+ *               stand at the last positions of the sequence: the last of
+ *               them at kv_lens[b] - 1.  A sequence may have none.  Rows
+ *               at or behind cu_tokens[B] belong to no sequence and are
+ *               left alone.
+ *   T           rows of the token arrays; T, B, kv_heads, max_pages,
+ *               num_pages >= 1; B <= 2^20; T * heads < 2^31
+ * page_table, kv_lens and cu_tokens are 4-byte aligned device arrays read by
+ * the kernels: their values are checked on the device.  A page outside
+ * 0..num_pages - 1 or a position outside 0..max_pages * page_size - 1 is never
+ * dereferenced: append drops the token, read gives zeros, attention leaves
+ * the keys out, and the next qz_device_status call reports
+ * QZ_ERR_DEVICE_INDEX.  Two tokens of one call must not share a place in the
+ * cache (two sequences may share pages that no call writes).
+ */
+QZ_API qz_status qz_kv4_cache_bytes(int64_t num_pages, int64_t kv_heads, int64_t head_dim,
+                                    int64_t page_size, int64_t group_size, size_t *bytes);
+
+/*
+ * Quantizes the keys and values of T new tokens into the cache.
+ * k, v: bf16, T rows of kv_heads * head_dim values, k_stride and v_stride
+ * elements apart (>= kv_heads * head_dim, multiples of 8), 16-byte aligned.
+ */
+QZ_API qz_status qz_kv4_append(void *cache, const void *k, const void *v, int64_t k_stride,
+                               int64_t v_stride, const void *page_table, const void *kv_lens,
+                               const void *cu_tokens, int64_t T, int64_t B, int64_t kv_heads,
+                               int64_t head_dim, int64_t page_size, int64_t group_size,
+                               int64_t num_pages, int64_t max_pages, void *stream);
+
+/*
+ * Reads the last cu_tokens[b + 1] - cu_tokens[b] cached tokens of every
+ * sequence back: k, v (T x kv_heads * head_dim bf16, row-major, 16-byte
+ * aligned) = bf16(S (q - Z)), as qz_dequantize forms them.
+ */
+QZ_API qz_status qz_kv4_read(const void *cache, const void *page_table, const void *kv_lens,
+                             const void *cu_tokens, int64_t T, int64_t B, int64_t kv_heads,
+                             int64_t head_dim, int64_t page_size, int64_t group_size,
+                             int64_t num_pages, int64_t max_pages, void *k, void *v,
+                             void *stream);
+
+/*
+ * Attention of T query rows over the cache: the query at position p of
+ * sequence b (head h, key head h / (q_heads / kv_heads)) gives
+ *   out = sum_j P_j v_j,  P = softmax_j(scale * q . k_j),
+ * over the keys j <= p and, when window > 0, j > p - window, with
+ * k_j = S (q - Z) and v_j likewise, not rounded.  A query without keys gives
+ * zeros.  Made for one or a few tokens a sequence (the keys are read once per
+ * 8 or 16 rows of T / B * q_heads / kv_heads); any number works.
+ * q: bf16, T rows of q_heads * head_dim, q_stride elements apart (a multiple
+ * of 8), 16-byte aligned.  out: the same with out_stride (2-byte aligned).
+ * q_heads % kv_heads == 0; scale finite; window >= 0 (0: none).
+ * fp32 softmax and sums; the weights P_j S_j are rounded to fp16 relative to
+ * their running maximum.  Results do not depend on timing.
+ * Workspace: qz_workspace_bytes(QZ_OP_KV4_ATTENTION, 1, 1, head_dim, 0)
+ * bytes, 256-byte aligned, zero-filled before its first use; each call that
+ * completes leaves its counters at zero again, whatever its sizes.  After
+ * QZ_ERR_DEVICE_TIMEOUT zero it again.
+ */
+QZ_API qz_status qz_kv4_attention(const void *q, int64_t q_stride, const void *cache,
+                                  const void *page_table, const void *kv_lens,
+                                  const void *cu_tokens, int64_t T, int64_t B, int64_t q_heads,
+                                  int64_t kv_heads, int64_t head_dim, int64_t page_size,
+                                  int64_t group_size, int64_t num_pages, int64_t max_pages,
+                                  float scale, int64_t window, void *out, int64_t out_stride,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Size of the scratch array built into the library for
  * qz_w4a16_gemv_noalloc (8 MiB, held on every GPU that loads the library).
  */
@@ -425,8 +523,10 @@ QZ_API qz_status qz_set_launch_overlap(int32_t mode);
 
 /*
  * Reads and clears the device error word of the current device (written by a
- * kernel whose bounded wait ran out).  Synchronizes the current device.
- * Returns QZ_OK or QZ_ERR_DEVICE_TIMEOUT (or QZ_ERR_CUDA).
+ * kernel whose bounded wait ran out, or that met a page or position out of
+ * range).  Synchronizes the current device.  Returns QZ_OK,
+ * QZ_ERR_DEVICE_TIMEOUT, QZ_ERR_DEVICE_INDEX (when no wait ran out) or
+ * QZ_ERR_CUDA.
  */
 QZ_API qz_status qz_device_status(void);
 

@@ -23,6 +23,8 @@ __all__ = [
     "qz_fp4_packed_bytes", "qz_fp4_quantize", "qz_fp4_dequantize", "qz_fp4a16_gemv",
     "QZ_OP_FP4A16_GEMV", "QZ_FP4_MX", "QZ_FP4_NV", "qz_fp4_mma_scale_bytes",
     "qz_fp4_scales_to_mma", "qz_fp4a4_gemm", "QZ_OP_FP4A4_GEMM",
+    "qz_kv4_cache_bytes", "qz_kv4_append", "qz_kv4_read", "qz_kv4_attention",
+    "QZ_OP_KV4_ATTENTION",
     "Workspace", "QZ_OP_QUANTIZE_PACK", "QZ_OP_DEQUANTIZE", "QZ_OP_W4A16_GEMV",
     "QZ_OP_W4A16_GEMM", "QZ_OP_W8A16_GEMV", "QZ_OP_W8A16_GEMM", "EXPORTED_SYMBOLS",
 ]
@@ -31,12 +33,15 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqz.so")
 
 QZ_OK = 0
 QZ_ERR_DEVICE_TIMEOUT = 6
+QZ_ERR_DEVICE_INDEX = 7
 (QZ_OP_QUANTIZE_PACK, QZ_OP_DEQUANTIZE, QZ_OP_W4A16_GEMV, QZ_OP_W4A16_GEMM, QZ_OP_W8A16_GEMV,
- QZ_OP_W8A16_GEMM, QZ_OP_GPTQ, QZ_OP_FP4A16_GEMV, QZ_OP_FP4A4_GEMM) = range(9)
+ QZ_OP_W8A16_GEMM, QZ_OP_GPTQ, QZ_OP_FP4A16_GEMV, QZ_OP_FP4A4_GEMM,
+ QZ_OP_KV4_ATTENTION) = range(10)
 QZ_FP4_MX, QZ_FP4_NV = 0, 1
 FP4_BLOCK = {QZ_FP4_MX: 32, QZ_FP4_NV: 16}
 
 _i32, _i64, _sz, _p = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
+_f32 = ctypes.c_float
 _SIGS = {
     "qz_status_string": ([ctypes.c_int], ctypes.c_char_p),
     "qz_version": ([], ctypes.c_int),
@@ -62,6 +67,11 @@ _SIGS = {
     "qz_fp4_mma_scale_bytes": ([_i64, _i64, _i32, ctypes.POINTER(_sz)], ctypes.c_int),
     "qz_fp4_scales_to_mma": ([_p, _i64, _i64, _i32, _p, _p], ctypes.c_int),
     "qz_fp4a4_gemm": ([_p, _p, _p, _p, _i64, _i64, _i64, _i32, _p, _p, _sz, _p], ctypes.c_int),
+    "qz_kv4_cache_bytes": ([_i64, _i64, _i64, _i64, _i64, ctypes.POINTER(_sz)], ctypes.c_int),
+    "qz_kv4_append": ([_p, _p, _p, _i64, _i64, _p, _p, _p] + [_i64] * 8 + [_p], ctypes.c_int),
+    "qz_kv4_read": ([_p, _p, _p, _p] + [_i64] * 8 + [_p, _p, _p], ctypes.c_int),
+    "qz_kv4_attention": ([_p, _i64, _p, _p, _p, _p] + [_i64] * 9 + [_f32, _i64, _p, _i64, _p, _sz,
+                                                                    _p], ctypes.c_int),
     "qz_set_device_wait_limit": ([ctypes.c_uint64], None),
     "qz_set_launch_overlap": ([ctypes.c_int32], ctypes.c_int),
     "qz_device_status": ([], ctypes.c_int),
@@ -448,6 +458,140 @@ def qz_fp4a4_gemm(a, codes, scales_mma, tensor_scale, N, K, kind, y=None, worksp
                                  workspace.numel() * workspace.element_size(), _handle(st)),
                "qz_fp4a4_gemm")
     return y
+
+
+# ---------------------------------------------------------------------------
+# paged 4-bit key/value cache
+# ---------------------------------------------------------------------------
+_KV4_BYTES = {}
+
+
+def qz_kv4_cache_bytes(num_pages, kv_heads, head_dim, page_size, group_size=128) -> int:
+    """Bytes of a cache of `num_pages` pages of `page_size` tokens (see qz.h)."""
+    key = (int(num_pages), int(kv_heads), int(head_dim), int(page_size), int(group_size))
+    v = _KV4_BYTES.get(key)
+    if v is None:
+        b = _sz()
+        _check(lib.qz_kv4_cache_bytes(*key, ctypes.byref(b)), "qz_kv4_cache_bytes")
+        v = _KV4_BYTES[key] = b.value
+    return v
+
+
+def _device_guard(dev):
+    """Makes `dev` current for a launch when it is not."""
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
+def _heads(t, name, dev):
+    """Pointer and token stride of a (T, heads, head_dim) bf16 tensor whose
+    heads and values are contiguous (tokens may lie further apart)."""
+    if t.dtype != torch.bfloat16 or t.dim() != 3:
+        raise ValueError(f"{name} must be a (tokens, heads, head_dim) bf16 tensor")
+    if t.device != dev or not t.is_cuda:
+        raise ValueError(f"{name} must live on the cache's CUDA device")
+    n, h, d = t.shape
+    st = t.stride()
+    if (d > 1 and st[2] != 1) or (h > 1 and st[1] != d):
+        raise ValueError(f"{name}: heads and values of a token must be contiguous")
+    return ctypes.c_void_p(t.data_ptr()), (st[0] if n > 1 else h * d)
+
+
+def _kv4_args(cache, page_table, kv_lens, cu_tokens, kv_heads, head_dim, page_size, group_size):
+    """Pointers of the four shared arrays, B, pages in the cache, pages per sequence."""
+    dev = cache.device
+    for t, name, dim in ((page_table, "page_table", 2), (kv_lens, "kv_lens", 1),
+                         (cu_tokens, "cu_tokens", 1)):
+        if t.dtype != torch.int32 or t.dim() != dim or t.device != dev:
+            raise ValueError(f"{name} must be a {dim}-D int32 tensor on the cache's device")
+    B = kv_lens.shape[0]
+    if page_table.shape[0] != B or cu_tokens.shape[0] != B + 1:
+        raise ValueError("page_table, kv_lens and cu_tokens must have B, B and B + 1 rows")
+    if cache.dtype != torch.uint8:
+        raise ValueError("cache must be a uint8 tensor")
+    pages = cache.numel() // qz_kv4_cache_bytes(1, kv_heads, head_dim, page_size, group_size)
+    return (_ptr(cache), _ptr(page_table), _ptr(kv_lens), _ptr(cu_tokens), B, pages,
+            page_table.shape[1])
+
+
+def qz_kv4_append(cache, k, v, page_table, kv_lens, cu_tokens, page_size, group_size=128,
+                  stream=None):
+    """Quantize new tokens' keys and values into the paged 4-bit cache.
+
+    cache: uint8 tensor of :func:`qz_kv4_cache_bytes` bytes; k, v: (T, kv_heads,
+    head_dim) bf16 (views of a fused projection are fine); page_table (B,
+    max_pages), kv_lens (B) and cu_tokens (B + 1): int32 tensors.  Tokens
+    cu_tokens[b]..cu_tokens[b + 1] - 1 become the last ones of sequence b, whose
+    length with them is kv_lens[b].
+    """
+    dev = cache.device
+    kp, ks = _heads(k, "k", dev)
+    vp, vs = _heads(v, "v", dev)
+    if k.shape != v.shape:
+        raise ValueError("k and v must have the same shape")
+    T, H, D = k.shape
+    c, pt, kl, cu, B, pages, width = _kv4_args(cache, page_table, kv_lens, cu_tokens, H, D,
+                                               page_size, group_size)
+    if T == 0:
+        return
+    st = _launch_stream(stream, dev)
+    with _device_guard(dev):
+        _check(lib.qz_kv4_append(c, kp, vp, ks, vs, pt, kl, cu, T, B, H, D, page_size, group_size,
+                                 pages, width, _handle(st)), "qz_kv4_append")
+
+
+def qz_kv4_read(cache, page_table, kv_lens, cu_tokens, tokens, kv_heads, head_dim, page_size,
+                group_size=128, k=None, v=None, stream=None):
+    """The last cu_tokens[b + 1] - cu_tokens[b] cached tokens of every sequence
+    as bf16: returns (k, v), each (tokens, kv_heads, head_dim)."""
+    dev = cache.device
+    c, pt, kl, cu, B, pages, width = _kv4_args(cache, page_table, kv_lens, cu_tokens, kv_heads,
+                                               head_dim, page_size, group_size)
+    shape = (tokens, kv_heads, head_dim)
+    for t in (k, v):
+        if t is not None and (t.dtype != torch.bfloat16 or tuple(t.shape) != shape or
+                              t.device != dev):
+            raise ValueError("k and v must be (tokens, kv_heads, head_dim) bf16 tensors")
+    st = _launch_stream(stream, dev)
+    with _on(stream), _device_guard(dev):
+        if k is None:
+            k = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        if v is None:
+            v = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        if tokens == 0:
+            return k, v
+        _check(lib.qz_kv4_read(c, pt, kl, cu, tokens, B, kv_heads, head_dim, page_size, group_size,
+                               pages, width, _ptr(k), _ptr(v), _handle(st)), "qz_kv4_read")
+    return k, v
+
+
+def qz_kv4_attention(q, cache, page_table, kv_lens, cu_tokens, kv_heads, page_size,
+                     group_size=128, scale=None, window=0, out=None, workspace=None, stream=None):
+    """Attention of (T, q_heads, head_dim) bf16 queries over the 4-bit cache
+    (causal; the queries of sequence b are its last tokens; `window` > 0 lets a
+    query see its last `window` keys).  scale defaults to head_dim ** -0.5."""
+    dev = cache.device
+    qp, qs = _heads(q, "q", dev)
+    T, H, D = q.shape
+    c, pt, kl, cu, B, pages, width = _kv4_args(cache, page_table, kv_lens, cu_tokens, kv_heads, D,
+                                               page_size, group_size)
+    st = _launch_stream(stream, dev)
+    with _on(stream), _device_guard(dev):
+        if out is None:
+            out = torch.empty((T, H, D), dtype=torch.bfloat16, device=dev)
+        elif out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+        if T == 0:
+            return out
+        op, os_ = _heads(out, "out", dev)
+        nbytes = qz_workspace_bytes(QZ_OP_KV4_ATTENTION, 1, 1, D, 0)
+        ws_ptr, ws_bytes = _ws_args(workspace, nbytes, dev, ("kv4_attention", D))
+        _check(lib.qz_kv4_attention(qp, qs, c, pt, kl, cu, T, B, H, kv_heads, D, page_size,
+                                    group_size, pages, width,
+                                    D ** -0.5 if scale is None else scale, window, op, os_,
+                                    ws_ptr, ws_bytes, _handle(st)), "qz_kv4_attention")
+    return out
 
 
 def qz_set_device_wait_limit(limit: int) -> None:

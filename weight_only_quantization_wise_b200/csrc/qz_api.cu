@@ -111,6 +111,7 @@ QZ_API const char *qz_status_string(int status) {
     case QZ_ERR_WORKSPACE: return "workspace missing or too small";
     case QZ_ERR_CUDA: return "CUDA call or kernel launch failed";
     case QZ_ERR_DEVICE_TIMEOUT: return "a bounded device-side wait ran out";
+    case QZ_ERR_DEVICE_INDEX: return "a page or position read on the device is out of range";
     default: return "unknown status";
     }
 }
@@ -179,6 +180,11 @@ QZ_API qz_status qz_workspace_bytes(int32_t op, int64_t M, int64_t N, int64_t K,
         *bytes = fp4a4_workspace_bytes(M, K);
         return QZ_OK;
     }
+    case QZ_OP_KV4_ATTENTION:
+        if (M < 1 || N < 1) return QZ_ERR_INVALID_ARG;
+        if (K != 64 && K != 128 && K != 256) return QZ_ERR_UNSUPPORTED;
+        *bytes = kv4_attention_workspace_bytes(K);
+        return QZ_OK;
     default:
         return QZ_ERR_INVALID_ARG;
     }
@@ -448,6 +454,109 @@ QZ_API qz_status qz_fp4a4_gemm(const void *a, const void *codes, const void *sca
     if (s != QZ_OK) return s;
     return launch_fp4a4_gemm(a, codes, scales_mma, tensor_scale, M, N, K, kind, y, workspace,
                              as_stream(stream));
+}
+
+namespace {
+
+// Sizes of the paged 4-bit cache; nothing of the shapes overflows once these hold.
+qz_status check_kv4_format(int64_t kv_heads, int64_t head_dim, int64_t page_size,
+                           int64_t group_size, int64_t num_pages) {
+    if (kv_heads < 1 || page_size < 1 || num_pages < 1 || head_dim < 1 || group_size < 1)
+        return QZ_ERR_INVALID_ARG;
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256) return QZ_ERR_UNSUPPORTED;
+    if (group_size != 32 && group_size != 64 && group_size != 128) return QZ_ERR_UNSUPPORTED;
+    if (group_size > head_dim || head_dim / group_size > 4) return QZ_ERR_UNSUPPORTED;
+    if (page_size % 16 != 0 || page_size > 65536) return QZ_ERR_UNSUPPORTED;
+    if (kv_heads > 65536 || num_pages > kMaxDim) return QZ_ERR_INVALID_ARG;
+    return QZ_OK;
+}
+
+qz_status check_kv4(const Kv4Cache &c, int64_t heads) {
+    const qz_status s =
+        check_kv4_format(c.kv_heads, c.head_dim, c.page_size, c.group_size, c.num_pages);
+    if (s != QZ_OK) return s;
+    if (c.T < 1 || c.B < 1 || c.max_pages < 1 || heads < 1) return QZ_ERR_INVALID_ARG;
+    if (c.T > kMaxDim || c.B > (int64_t(1) << 20) || c.max_pages > kMaxDim || heads > 65536 ||
+        c.T * heads > kMaxDim)
+        return QZ_ERR_INVALID_ARG;
+    if (!c.cache || !c.page_table || !c.kv_lens || !c.cu) return QZ_ERR_INVALID_ARG;
+    if (!aligned(c.cache, 16) || !aligned(c.page_table, 4) || !aligned(c.kv_lens, 4) ||
+        !aligned(c.cu, 4))
+        return QZ_ERR_ALIGNMENT;
+    return QZ_OK;
+}
+
+// Rows of `width` elements `stride` apart, read or written `vec` elements at a time.
+qz_status check_rows(int64_t stride, int64_t width, int64_t vec) {
+    if (stride < width || stride > kMaxElems) return QZ_ERR_INVALID_ARG;
+    return stride % vec == 0 ? QZ_OK : QZ_ERR_ALIGNMENT;
+}
+
+}  // namespace
+
+QZ_API qz_status qz_kv4_cache_bytes(int64_t num_pages, int64_t kv_heads, int64_t head_dim,
+                                    int64_t page_size, int64_t group_size, size_t *bytes) {
+    if (!bytes) return QZ_ERR_INVALID_ARG;
+    const qz_status s = check_kv4_format(kv_heads, head_dim, page_size, group_size, num_pages);
+    if (s != QZ_OK) return s;
+    const size_t page = (size_t)kv_heads * (size_t)(page_size / 16) *
+                        kv4_record_bytes(head_dim, group_size);
+    if ((size_t)num_pages > ((size_t)1 << 60) / page) return QZ_ERR_INVALID_ARG;
+    *bytes = (size_t)num_pages * page;
+    return QZ_OK;
+}
+
+QZ_API qz_status qz_kv4_append(void *cache, const void *k, const void *v, int64_t k_stride,
+                               int64_t v_stride, const void *page_table, const void *kv_lens,
+                               const void *cu_tokens, int64_t T, int64_t B, int64_t kv_heads,
+                               int64_t head_dim, int64_t page_size, int64_t group_size,
+                               int64_t num_pages, int64_t max_pages, void *stream) {
+    const Kv4Cache c{cache,    page_table, kv_lens,   cu_tokens, T, B, kv_heads, head_dim,
+                     group_size, page_size, num_pages, max_pages};
+    qz_status s = check_kv4(c, kv_heads);
+    if (s != QZ_OK) return s;
+    if (!k || !v) return QZ_ERR_INVALID_ARG;
+    if (!aligned(k, 16) || !aligned(v, 16)) return QZ_ERR_ALIGNMENT;
+    if ((s = check_rows(k_stride, kv_heads * head_dim, 8)) != QZ_OK) return s;
+    if ((s = check_rows(v_stride, kv_heads * head_dim, 8)) != QZ_OK) return s;
+    return launch_kv4_append(c, k, v, k_stride, v_stride, as_stream(stream));
+}
+
+QZ_API qz_status qz_kv4_read(const void *cache, const void *page_table, const void *kv_lens,
+                             const void *cu_tokens, int64_t T, int64_t B, int64_t kv_heads,
+                             int64_t head_dim, int64_t page_size, int64_t group_size,
+                             int64_t num_pages, int64_t max_pages, void *k, void *v,
+                             void *stream) {
+    const Kv4Cache c{const_cast<void *>(cache), page_table, kv_lens,   cu_tokens, T, B, kv_heads,
+                     head_dim, group_size, page_size, num_pages, max_pages};
+    const qz_status s = check_kv4(c, kv_heads);
+    if (s != QZ_OK) return s;
+    if (!k || !v) return QZ_ERR_INVALID_ARG;
+    if (!aligned(k, 16) || !aligned(v, 16)) return QZ_ERR_ALIGNMENT;
+    return launch_kv4_read(c, k, v, as_stream(stream));
+}
+
+QZ_API qz_status qz_kv4_attention(const void *q, int64_t q_stride, const void *cache,
+                                  const void *page_table, const void *kv_lens,
+                                  const void *cu_tokens, int64_t T, int64_t B, int64_t q_heads,
+                                  int64_t kv_heads, int64_t head_dim, int64_t page_size,
+                                  int64_t group_size, int64_t num_pages, int64_t max_pages,
+                                  float scale, int64_t window, void *out, int64_t out_stride,
+                                  void *workspace, size_t workspace_bytes, void *stream) {
+    const Kv4Cache c{const_cast<void *>(cache), page_table, kv_lens,   cu_tokens, T, B, kv_heads,
+                     head_dim, group_size, page_size, num_pages, max_pages};
+    qz_status s = check_kv4(c, q_heads);
+    if (s != QZ_OK) return s;
+    if (q_heads % kv_heads != 0 || window < 0) return QZ_ERR_INVALID_ARG;
+    if (!(scale > -1e30f && scale < 1e30f)) return QZ_ERR_INVALID_ARG;
+    if (!q || !out) return QZ_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(out, 2)) return QZ_ERR_ALIGNMENT;
+    if ((s = check_rows(q_stride, q_heads * head_dim, 8)) != QZ_OK) return s;
+    if ((s = check_rows(out_stride, q_heads * head_dim, 1)) != QZ_OK) return s;
+    s = check_workspace(kv4_attention_workspace_bytes(head_dim), workspace, workspace_bytes);
+    if (s != QZ_OK) return s;
+    return launch_kv4_attention(c, q, q_stride, q_heads, scale, window, out, out_stride, workspace,
+                                as_stream(stream));
 }
 
 }  // extern "C"

@@ -49,7 +49,8 @@
 
 namespace qz {
 
-// Set (atomicOr) by a kernel whose bounded wait ran out.
+// Set (atomicOr) by a kernel whose bounded wait ran out (bit 0) or that met
+// an index out of range (bit 1).
 __device__ unsigned int g_device_error_word = 0;
 
 namespace {
@@ -1036,5 +1037,5 @@ extern "C" QZ_API qz_status qz_device_status(void) {
     const unsigned int zero = 0;
     if (cudaMemcpyToSymbol(qz::g_device_error_word, &zero, sizeof zero) != cudaSuccess)
         return QZ_ERR_CUDA;
-    return QZ_ERR_DEVICE_TIMEOUT;
+    return (word & 1u) ? QZ_ERR_DEVICE_TIMEOUT : QZ_ERR_DEVICE_INDEX;
 }

@@ -170,6 +170,21 @@ qz_status launch_gptq(const void *w, const void *x, int64_t N, int64_t K, int64_
                       int bits, int symmetric, int64_t group_size, double damp, void *codes,
                       void *scales, void *zeros, void *workspace, cudaStream_t stream);
 
+// The paged 4-bit key/value cache (qz_kv4.cu).
+struct Kv4Cache {
+    void *cache;
+    const void *page_table, *kv_lens, *cu;     // int32 [B][max_pages], [B], [B + 1]
+    int64_t T, B, kv_heads, head_dim, group_size, page_size, num_pages, max_pages;
+};
+size_t kv4_record_bytes(int64_t head_dim, int64_t group_size);
+size_t kv4_attention_workspace_bytes(int64_t head_dim);
+qz_status launch_kv4_append(const Kv4Cache &c, const void *k, const void *v, int64_t k_stride,
+                            int64_t v_stride, cudaStream_t stream);
+qz_status launch_kv4_read(const Kv4Cache &c, void *k, void *v, cudaStream_t stream);
+qz_status launch_kv4_attention(const Kv4Cache &c, const void *q, int64_t q_stride, int64_t q_heads,
+                               float scale, int64_t window, void *out, int64_t out_stride,
+                               void *workspace, cudaStream_t stream);
+
 uint64_t device_wait_limit();
 // qz_set_launch_overlap mode (0 or 1) for the decode GEMV launches.
 int32_t launch_overlap();

@@ -1,0 +1,140 @@
+// qz_kv4_index.cuh -- index arithmetic of the paged 4-bit key/value cache and
+// of the attention's work split.  Plain C++ for host and device: the kernels
+// use it, and the CPU tests compile it with the host compiler and check every
+// index and range it gives.
+//
+// Cache layout.  A page holds `page_size` tokens (a multiple of 16) of every
+// key head: [page][kv head][page_size / 16][record].  A record is everything
+// attention needs of 16 consecutive tokens of one head, contiguous and a
+// multiple of 16 bytes, so that one untiled bulk copy brings it to shared
+// memory:
+//   K codes   8 D bytes     V codes   8 D bytes
+//   K scales  [D/g][16] bf16    V scales  [D/g][16] bf16
+//   K zeros   [D/g][16] uint8   V zeros   [D/g][16] uint8
+// The codes lie as the lanes of a warp read them for mma.sync m16n8k16 (lane
+// = 4 * gid + tid, gid 0..7, tid 0..3): "piece" i holds four 32-bit words of
+// each of the 32 lanes, 16 bytes per lane, so every shared-memory load is one
+// 16-byte load free of bank conflicts.
+//   K (A operand, tokens x d): lane (gid, tid) reads tokens gid and gid + 8;
+//     word (hi, j) holds the eight codes d = 32 j + 8 tid + n (nibble n) of
+//     token 8 hi + gid.  Word number hi * (D / 32) + j.
+//   V (A operand, d x tokens): word (p, hi, w) of lane (gid, tid) holds for
+//     tokens 8 p + 2 tid (low half) and 8 p + 2 tid + 1 (high half) the four
+//     codes d = 64 w + 16 n + 8 hi + gid (nibble n of the half).  Word number
+//     p * (D / 32) + hi * (D / 64) + w.
+#pragma once
+
+#include <stdint.h>
+
+#if defined(__CUDACC__)
+#define QZ_HD __host__ __device__ __forceinline__
+#else
+#define QZ_HD inline
+#endif
+
+namespace qz {
+namespace kv4 {
+
+constexpr int kBlock = 16;     // tokens of a record
+
+// ---- record -------------------------------------------------------------
+QZ_HD constexpr int64_t record_bytes(int64_t D, int64_t g) { return 16 * D + 96 * (D / g); }
+QZ_HD constexpr int k_codes_off() { return 0; }
+QZ_HD constexpr int v_codes_off(int D) { return 8 * D; }
+QZ_HD constexpr int k_scales_off(int D) { return 16 * D; }
+QZ_HD constexpr int v_scales_off(int D, int ng) { return 16 * D + 32 * ng; }
+QZ_HD constexpr int k_zeros_off(int D, int ng) { return 16 * D + 64 * ng; }
+QZ_HD constexpr int v_zeros_off(int D, int ng) { return 16 * D + 80 * ng; }
+
+// Byte of word `word` of lane (gid, tid) within a code area.
+QZ_HD constexpr int word_byte(int word, int gid, int tid) {
+    return ((word >> 2) * 32 + 4 * gid + tid) * 16 + (word & 3) * 4;
+}
+// K: byte of the 32-bit word holding codes 8 c8 .. 8 c8 + 7 of a token.
+QZ_HD constexpr int k_word_byte(int D, int token, int c8) {
+    return word_byte((token >> 3) * (D / 32) + (c8 >> 2), token & 7, c8 & 3);
+}
+// V: byte of the 16-bit unit of a token holding the codes
+// d = 64 w + 16 n + 8 hi + gid, n = 0..3 (nibble n).
+QZ_HD constexpr int v_unit_byte(int D, int token, int w, int hi, int gid) {
+    return word_byte((token >> 3) * (D / 32) + hi * (D / 64) + w, gid, (token & 7) >> 1) +
+           2 * (token & 1);
+}
+
+// ---- pages --------------------------------------------------------------
+// Record index (in records from the cache's start) of the block of 16 tokens
+// that holds position `pos` of head `h`, or -1 when the page table has no
+// valid page there.  `row` is the sequence's row of the page table.
+QZ_HD int64_t record_index(const int32_t *row, int64_t max_pages, int64_t num_pages,
+                           int64_t kv_heads, int64_t h, int page_blocks, int64_t block) {
+    const int64_t pi = block / page_blocks;
+    if (block < 0 || pi >= max_pages) return -1;
+    const int32_t page = row[pi];
+    if (page < 0 || page >= num_pages) return -1;
+    return ((int64_t)page * kv_heads + h) * page_blocks + (block - pi * page_blocks);
+}
+
+// Sequence that owns token t: the b with cu[b] <= t < cu[b + 1]; -1 when no
+// sequence does (tokens behind the last one).
+QZ_HD int64_t find_sequence(const int32_t *cu, int64_t B, int64_t t) {
+    int64_t lo = 0, hi = B;                   // first b with cu[b + 1] > t
+    while (lo < hi) {
+        const int64_t mid = (lo + hi) >> 1;
+        if ((int64_t)cu[mid + 1] > t) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo < B && (int64_t)cu[lo] <= t ? lo : -1;
+}
+
+// ---- attention's work ---------------------------------------------------
+// A sequence with n new tokens (queries) and len cached tokens (the new ones
+// included) has n * share query rows per key head (share = query heads per
+// key head), in tiles of `tile_rows`.  An item is one (key head, row tile);
+// its units are the blocks of 16 keys [block0, block0 + blocks) that any of
+// the sequence's rows may see.  Every item has at least one unit, so that
+// rows without keys are written too.
+struct SeqWork {
+    int64_t n, len;       // queries, keys
+    int64_t block0;       // first block of keys
+    int64_t blocks;       // units of an item (>= 1)
+    int64_t row_tiles;    // row tiles per key head
+    int64_t units;        // kv_heads * row_tiles * blocks (0 when n == 0)
+};
+
+QZ_HD SeqWork seq_work(int64_t cu0, int64_t cu1, int64_t kv_len, int64_t capacity, int64_t window,
+                       int64_t share, int64_t kv_heads, int64_t tile_rows) {
+    SeqWork s;
+    s.n = cu1 > cu0 ? cu1 - cu0 : 0;
+    s.len = kv_len < 0 ? 0 : (kv_len > capacity ? capacity : kv_len);
+    int64_t first = window > 0 ? s.len - s.n - window + 1 : 0;
+    if (first < 0) first = 0;
+    s.block0 = first / kBlock;
+    const int64_t end = (s.len + kBlock - 1) / kBlock;
+    s.blocks = end - s.block0 > 1 ? end - s.block0 : 1;
+    s.row_tiles = (s.n * share + tile_rows - 1) / tile_rows;
+    s.units = s.row_tiles * kv_heads * s.blocks;
+    return s;
+}
+
+// The units of all items, in (sequence, head, row tile, block) order, are cut
+// into equal contiguous ranges, one per worker.
+QZ_HD int64_t range_begin(int64_t c, int64_t units, int64_t workers) {
+    return c * units / workers;
+}
+// First worker whose range holds unit u.
+QZ_HD int64_t worker_of(int64_t u, int64_t units, int64_t workers) {
+    return ((u + 1) * workers - 1) / units;
+}
+// CTAs that take part: as many as there are, unless that leaves one fewer
+// than min_units units.
+QZ_HD int64_t active_ctas(int64_t units, int64_t ctas, int64_t min_units) {
+    const int64_t most = (units + min_units - 1) / min_units;
+    return most < ctas ? (most < 1 ? 1 : most) : ctas;
+}
+// Partial results in the workspace: a CTA has two slots, 0 for an item that
+// is under way where its range begins (or begins there), 1 for one that
+// begins inside its range and goes on in the next CTA.
+QZ_HD int partial_slot(int64_t item_begin, int64_t cta_begin) { return item_begin > cta_begin; }
+
+}  // namespace kv4
+}  // namespace qz
