@@ -32,13 +32,14 @@ ll s_record_index(const int *row, ll max_pages, ll num_pages, ll heads, ll h, in
     return record_index(row, max_pages, num_pages, heads, h, pb, block);
 }
 ll s_find_sequence(const int *cu, ll B, ll t) { return find_sequence(cu, B, t); }
-void s_seq_work(ll cu0, ll cu1, ll len, ll cap, ll win, ll share, ll heads, ll rows, ll *o) {
-    const SeqWork s = seq_work(cu0, cu1, len, cap, win, share, heads, rows);
+void s_seq_work(int cu0, int cu1, int len, int T, int cap, int win, int share, int heads, int rows,
+                ll *o) {
+    const SeqWork s = seq_work(cu0, cu1, len, T, cap, win, share, heads, rows);
     o[0] = s.n; o[1] = s.len; o[2] = s.block0; o[3] = s.blocks; o[4] = s.row_tiles; o[5] = s.units;
 }
-ll s_range_begin(ll c, ll u, ll w) { return range_begin(c, u, w); }
-ll s_worker_of(ll u, ll units, ll w) { return worker_of(u, units, w); }
-ll s_active_ctas(ll u, ll c, ll m) { return active_ctas(u, c, m); }
+ll s_range_begin(ll c, ll q, ll u) { return range_begin(c, q, u); }
+ll s_cta_quota(ll u, ll c, ll m) { return cta_quota(u, c, m); }
+int s_warp_quota(ll n, int w) { return warp_quota(n, w); }
 int s_partial_slot(ll a, ll b) { return partial_slot(a, b); }
 }
 """
@@ -56,11 +57,11 @@ def ix(tmp_path_factory):
     ll = ctypes.c_longlong
     for name, args in (("s_record_index", [ctypes.c_void_p, ll, ll, ll, ll, ctypes.c_int, ll]),
                        ("s_find_sequence", [ctypes.c_void_p, ll, ll]),
-                       ("s_range_begin", [ll, ll, ll]), ("s_worker_of", [ll, ll, ll]),
-                       ("s_active_ctas", [ll, ll, ll])):
+                       ("s_range_begin", [ll, ll, ll]), ("s_cta_quota", [ll, ll, ll])):
         f = getattr(so, name)
         f.argtypes, f.restype = args, ll
-    so.s_seq_work.argtypes = [ll] * 8 + [ctypes.c_void_p]
+    so.s_seq_work.argtypes = [ctypes.c_int] * 9 + [ctypes.c_void_p]
+    so.s_warp_quota.argtypes = [ll, ctypes.c_int]
     so.s_partial_slot.argtypes = [ll, ll]
     return so
 
@@ -161,10 +162,10 @@ def test_work_split(ix, case):
     is counted at a CTA that counts no other item; every key that a row sees
     lies in a unit."""
     lens, new, window, share, heads, rows, grid, min_units, warps = list(batches())[case]
-    items, cu = [], 0
+    items, cu, T = [], 0, max(1, sum(new))
     for L, n in zip(lens, new):
         o = (ctypes.c_longlong * 6)()
-        ix.s_seq_work(cu, cu + n, L, 4096, window, share, heads, rows, o)
+        ix.s_seq_work(cu, cu + n, L, T, 4096, window, share, heads, rows, o)
         cu += n
         assert o[0] == n and o[1] == L and o[5] == o[4] * heads * o[3]
         assert o[4] == -(-n * share // rows)
@@ -178,21 +179,19 @@ def test_work_split(ix, case):
     if units == 0:
         return
     begins = np.cumsum([0] + items)
-    ctas = ix.s_active_ctas(units, grid, min_units)
-    assert 1 <= ctas <= min(grid, units)
-    covered, homes, slots = 0, {}, {}
-    for c in range(ctas):
-        b0, b1 = ix.s_range_begin(c, units, ctas), ix.s_range_begin(c + 1, units, ctas)
-        assert b0 == covered and b1 > b0
-        for u in {b0, (b0 + b1) // 2, b1 - 1}:
-            assert ix.s_worker_of(u, units, ctas) == c
-        at = b0
-        for w in range(warps):
-            w0 = b0 + ix.s_range_begin(w, b1 - b0, warps)
-            w1 = b0 + ix.s_range_begin(w + 1, b1 - b0, warps)
-            assert w0 == at and w1 >= w0
-            at = w1
-        assert at == b1
+    quota = ix.s_cta_quota(units, grid, min_units)
+    assert quota >= min_units and quota * grid >= units
+    covered, homes, slots, active = 0, {}, {}, 0
+    for c in range(grid):
+        b0, b1 = ix.s_range_begin(c, quota, units), ix.s_range_begin(c + 1, quota, units)
+        if b0 >= b1:
+            assert b0 == units
+            continue
+        assert b0 == covered and c == active
+        active += 1
+        assert all(u // quota == c for u in (b0, (b0 + b1) // 2, b1 - 1))
+        wq = ix.s_warp_quota(b1 - b0, warps)
+        assert wq % 2 == 0 and wq * warps >= b1 - b0
         covered = b1
         first = int(np.searchsorted(begins, b0, "right") - 1)
         last = int(np.searchsorted(begins, b1 - 1, "right") - 1)
@@ -200,20 +199,32 @@ def test_work_split(ix, case):
             i0, i1 = int(begins[it]), int(begins[it + 1])
             if i0 >= b0 and i1 <= b1:
                 continue
-            home = ix.s_worker_of(i0, units, ctas)
+            home = i0 // quota
             assert homes.setdefault(home, it) == it
             slot = ix.s_partial_slot(i0, b0)
             assert (c, slot) not in slots
             slots[(c, slot)] = it
             # how the last to arrive finds this part
-            c0 = home
-            s0 = ix.s_partial_slot(i0, ix.s_range_begin(c0, units, ctas))
-            assert slot == (s0 if c == c0 else 0)
+            s0 = ix.s_partial_slot(i0, ix.s_range_begin(home, quota, units))
+            assert slot == (s0 if c == home else 0)
     assert covered == units
     for home, it in homes.items():
-        c0 = home
-        c1 = ix.s_worker_of(int(begins[it + 1]) - 1, units, ctas)
-        assert sorted(c for (c, _), i in slots.items() if i == it) == list(range(c0, c1 + 1))
+        c1 = (int(begins[it + 1]) - 1) // quota
+        assert sorted(c for (c, _), i in slots.items() if i == it) == list(range(home, c1 + 1))
+
+
+def test_wild_lengths_and_offsets_stay_in_range(ix):
+    """Values no caller should pass: work counts stay non-negative and bounded."""
+    big = 2 ** 31 - 1
+    for cu0, cu1, L in [(0, big, 5), (-big, 5, 5), (5, 0, 5), (-1, 3, 5), (0, 1, -big), (0, 1, big),
+                        (big - 1, big, big)]:
+        for window in (0, 1, 1000):
+            o = (ctypes.c_longlong * 6)()
+            ix.s_seq_work(cu0, cu1, L, 100, 2 ** 31 - 32, window, 16, 8, 8, o)
+            n, length, block0, blocks, tiles, units = o
+            assert 0 <= n <= 100 and 0 <= length <= 2 ** 31 - 32 and blocks >= 1
+            assert 0 <= block0 and (block0 + blocks) * 16 < 2 ** 31
+            assert tiles == -(-n * 16 // 8) and units == tiles * 8 * blocks
 
 
 # ---------------------------------------------------------------------------
@@ -298,11 +309,11 @@ def test_kv4_sizes():
         qz.qz_kv4_cache_bytes(7, 3, 128, 40, 128)
     with pytest.raises(qz.QzError):
         qz.qz_kv4_cache_bytes(2 ** 31 - 1, 65536, 256, 65536, 64)
-    # two slots of 16 rows (head_dim + 4 fp32, 4 fp32 per row) and a counter
+    # two slots of 16 rows (head_dim + 4 fp32, 2 fp32 per row) and a counter
     # for each of 2 x 148 CTAs
     for D in (64, 128, 256):
         assert (qz.qz_workspace_bytes(qz.QZ_OP_KV4_ATTENTION, 1, 1, D, 0) ==
-                1280 + 296 * 2 * 16 * (D + 8) * 4)
+                1280 + 296 * 2 * 16 * (D + 6) * 4)
     with pytest.raises(qz.QzError):
         qz.qz_workspace_bytes(qz.QZ_OP_KV4_ATTENTION, 1, 1, 96, 0)
     assert qz.qz_status_string(qz.QZ_ERR_DEVICE_INDEX) != "unknown status"

@@ -223,72 +223,91 @@ __global__ void __launch_bounds__(32 * kStoreWarps) kv4_read_kernel(const StoreA
 // 2^-15 of the largest product, seen where one key holds the weight and c = Z.)
 // Queries are bf16 brought into fp16's range by a power of two per row (exact
 // above 2^-24 of the row's largest value).  S stays out of the first product.
-// Weights P_j S_j are rounded once to fp16 (relative 2^-12) for the second
-// product, scaled by 2^-n, n a running maximum of s_j + log2 of S_j's binade
-// beside the softmax's running maximum m of s_j (both in powers of two), so
-// that they lie in (0, 2^5) whatever the sizes of V.
-// Sums, maxima and partial results are fp32.
+// The weights w_j = P_j S_j are rounded once to fp16 (2^-11 of each) for the
+// second product.  One running maximum n per row, of s_j + log2 S_j (all in
+// powers of two), scales both sums: w_j = 2^(s_j - n) S_j lies below 2^4
+// whatever the sizes of V, and the softmax's sum l of 2^(s_j - n) is fp32; the
+// result is the quotient of the two sums.  log2 S_j is kept within -+100, so
+// that l neither overflows nor vanishes.
+//
+// Work.  Warps work alone: a warp takes a contiguous range of (head, block)
+// units, keeps records of 16 tokens in a ring of its own (two per stage, one
+// bulk copy each) and its sums in registers, 8 NB query rows as the columns
+// of the tensor-core tiles (tokens x heads for the scores, d x heads for the
+// result, so that the probabilities only need an 8 x 8 transpose between the
+// two).  An item cut by warps is joined in shared memory, one cut by CTAs in
+// the workspace by the last to arrive, parts added in order.
 struct AttnArgs {
     const uint16_t *q;
     int64_t q_stride;                  // elements between tokens
     const uint8_t *cache;
     const int32_t *page_table, *kv_lens, *cu;
-    int64_t T, B, max_pages, num_pages, window, capacity;
-    int kv_heads, share, page_blocks;
+    int64_t max_pages, num_pages;
+    int T, B, window, capacity, kv_heads, share, page_blocks;
     float scale_log2;                  // scale * log2(e)
     uint16_t *out;
     int64_t out_stride;
     float *partials;                   // [ctas][2][Slot]
     uint32_t *counters;                // [ctas]
-    int64_t min_units;
+    int min_units;
     uint64_t wait_limit;
     unsigned int *err_word;
 };
 
 constexpr float kNoMax = -1e30f;       // running maximum before any key
 
-// A partial result of a row tile: [R][D + 4] fp32 sums, then m, n, l per row.
+// A partial result of a row tile: [R][D + 4] fp32 sums, then n and l per row.
 template <int D, int NB>
 struct Slot {
     static constexpr int R = 8 * NB;
     static constexpr int pitch = D + 4;                    // floats: rows 8 apart in banks
-    static constexpr int stats = R * pitch;                // [3][R]
-    static constexpr int floats = R * pitch + 4 * R;
+    static constexpr int stats = R * pitch;                // n[R], l[R]
+    static constexpr int floats = R * pitch + 2 * R;
     static constexpr int bytes = floats * 4;
 };
 
-// Dynamic shared memory of a CTA so that two fit on an SM (228 KB, 1 KB of it
-// reserved per CTA, and up to 3 KB of static arrays).
-constexpr int kAttnSmem = 110 * 1024;
+// Dynamic shared memory of a CTA: 228 KB per SM, 1 KB of it reserved per CTA,
+// and up to 5 KB of static arrays.
+constexpr int attn_smem(int ctas) { return (ctas == 2 ? 108 : 221) * 1024; }
 
-template <int D, int G, int NB, int WARPS>
+template <int D, int G, int NB, int WARPS, int CTAS>
 struct AttnLayout {
     static constexpr int NG = D / G;
+    static constexpr bool q_smem = D == 256 && NB == 2;    // queries do not fit in registers
     static constexpr int rec = (int)record_bytes(D, G);
     static constexpr int slot = Slot<D, NB>::bytes;
-    static constexpr int ring_bytes(int s) { return ((s * rec > slot ? s * rec : slot) + 15) & ~15; }
-    static constexpr int total(int s) { return WARPS * (ring_bytes(s) + slot + 8 * s); }
-    // records in flight per warp: up to 6, as many as let two CTAs share an SM
-    static constexpr int S = total(6) <= kAttnSmem ? 6 : total(5) <= kAttnSmem ? 5
-                             : total(4) <= kAttnSmem ? 4 : 3;
+    static constexpr int q_bytes = q_smem ? 8 * NB * D * 2 : 0;
+    static constexpr int ring_bytes(int s) {
+        return ((2 * s * rec > slot ? 2 * s * rec : slot) + 15) & ~15;
+    }
+    static constexpr int total(int s) { return WARPS * (ring_bytes(s) + slot + q_bytes + 8 * s); }
+    // stages (two records each) in flight per warp
+    static constexpr int S = total(3) <= attn_smem(CTAS) ? 3 : 2;
     static constexpr int ring = ring_bytes(S);
-    static constexpr int ring_off = 0;                     // [WARPS][ring]; later slot 1
-    static constexpr int first_off = WARPS * ring;         // [WARPS][slot]: slot 0
-    static constexpr int bars_off = first_off + WARPS * slot;
+    static constexpr int ring_off = 0;                     // [WARPS][ring]; later part 1 of a warp
+    static constexpr int first_off = WARPS * ring;         // [WARPS][slot]: part 0
+    static constexpr int q_off = first_off + WARPS * slot;
+    static constexpr int bars_off = q_off + WARPS * q_bytes;
     static constexpr int bytes = bars_off + WARPS * S * 8;
-    static_assert(bytes <= kAttnSmem, "two CTAs fit on an SM");
+    static_assert(bytes <= attn_smem(CTAS), "the CTAs fit on an SM");
     static_assert(rec % 16 == 0 && slot % 16 == 0, "bulk copies and slots are 16-byte aligned");
+    // the last to arrive keeps a factor per part and row in the ring area
+    static_assert(WARPS * ring >= kSmCount * 2 * 8 * NB * 4, "factors of all parts fit");
 };
 
-struct Part {                          // a warp's partial result of an item
+struct Part {                          // a warp's part of an item
     int64_t item_begin, item_end;      // units; item_end = 0: none
-    int64_t b;
-    int h, rt;
+    int b, h, rt;
 };
 
 __device__ __forceinline__ float ex2(float x) {
     float r;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float lg2(float x) {
+    float r;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -345,64 +364,43 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_
         ::"r"(dst), "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar) : "memory");
 }
 
-// Where row `row` of a sequence (head h of the key heads) lies: its token,
-// or -1 when the row does not exist or its token is not among the T.
-__device__ __forceinline__ int64_t row_token(int64_t row, int64_t n, int share, int64_t cu0,
-                                             int64_t T) {
-    if (row >= n * share) return -1;
-    const int64_t tok = cu0 + row / share;
-    return tok >= 0 && tok < T ? tok : -1;
+// mbar_wait that reads the clock only after 64 polls (each may suspend the
+// warp for up to a microsecond): the waits here are short and frequent.
+__device__ __forceinline__ bool ring_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns,
+                                          volatile uint32_t *abort_flag, unsigned int *err_word) {
+    if (mbar_try_wait(bar, parity)) return true;
+    for (int i = 0; i < 64; ++i)
+        if (mbar_try_wait_hint(bar, parity, 1000u)) return true;
+    return mbar_wait(bar, parity, limit_ns, abort_flag, err_word);
 }
 
-// What a row's sums are multiplied with at the end: 2^(nm - m) / l; 0 for a
-// row that saw no key, NaN when l is.
-__device__ __forceinline__ float row_factor(float m, float nm, float l) {
-    return l > 0.0f ? ex2(nm - m) / l : l;
+// Output row of query row `row` of item (b, h), or null when there is none.
+template <int D>
+__device__ __forceinline__ uint16_t *out_row(const AttnArgs &p, int cu0, int n, int h, int row) {
+    if (row >= n * p.share) return nullptr;
+    const int i = row / p.share, tok = cu0 + i;
+    if (tok < 0 || tok >= p.T) return nullptr;
+    return p.out + (int64_t)tok * p.out_stride + (int64_t)(h * p.share + row - i * p.share) * D;
 }
 
-// Adds the `count` partial results part(0), part(1), ... of an item in that
-// order, all threads of the CTA: into the partial result `dst` when it is not
-// null, else normalised into the output.
-template <int D, int NB, bool GLOBAL, typename F>
-__device__ __forceinline__ void merge_parts(const AttnArgs &p, F part, int count, float *dst,
-                                            const Part &it, int tid, int threads) {
-    using L = Slot<D, NB>;
-    const int64_t cu0 = p.cu[it.b], n = (int64_t)p.cu[it.b + 1] - cu0;
-    auto ld = [](const float *q) { return GLOBAL ? __ldcg(q) : *q; };
-    for (int e = tid; e < L::R * D; e += threads) {
-        const int row = e / D, d = e - row * D;
-        float m = kNoMax, nm = kNoMax;
-        for (int i = 0; i < count; ++i) {
-            const float *s = part(i) + L::stats + row;
-            m = fmaxf(m, ld(s));
-            nm = fmaxf(nm, ld(s + L::R));
-        }
-        float l = 0.0f, o = 0.0f;
-        for (int i = 0; i < count; ++i) {
-            const float *q = part(i), *s = q + L::stats + row;
-            l += ld(s + 2 * L::R) * ex2(ld(s) - m);
-            o += ld(q + row * L::pitch + d) * ex2(ld(s + L::R) - nm);
-        }
-        if (dst) {
-            __stcg(dst + row * L::pitch + d, o);
-            if (d == 0) {
-                __stcg(dst + L::stats + row, m);
-                __stcg(dst + L::stats + L::R + row, nm);
-                __stcg(dst + L::stats + 2 * L::R + row, l);
-            }
-        } else {
-            const int64_t r = (int64_t)it.rt * L::R + row;
-            const int64_t tok = row_token(r, n, p.share, cu0, p.T);
-            if (tok >= 0)
-                p.out[tok * p.out_stride + ((int64_t)it.h * p.share + r % p.share) * D + d] =
-                    (uint16_t)dev::f32_to_bf16_rne(o * row_factor(m, nm, l));
-        }
+// Four results of a row (8-byte store where the row allows it).
+__device__ __forceinline__ void store4(uint16_t *dst, float4 o, float f) {
+    const uint32_t a = dev::pack_bf16x2(o.x * f, o.y * f), b = dev::pack_bf16x2(o.z * f, o.w * f);
+    if ((reinterpret_cast<uintptr_t>(dst) & 7) == 0) {
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(a, b);
+    } else {
+        dst[0] = (uint16_t)a; dst[1] = (uint16_t)(a >> 16);
+        dst[2] = (uint16_t)b; dst[3] = (uint16_t)(b >> 16);
     }
 }
 
+// What a row's sums are multiplied with at the end: 1 / l; 0 for a row that
+// saw no key, NaN when l is.
+__device__ __forceinline__ float row_factor(float l) { return l > 0.0f ? 1.0f / l : l; }
+
 template <int D, int G, int NB, int WARPS, int CTAS>
 __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const AttnArgs p) {
-    using L = AttnLayout<D, G, NB, WARPS>;
+    using L = AttnLayout<D, G, NB, WARPS, CTAS>;
     using SL = Slot<D, NB>;
     constexpr int NG = L::NG, S = L::S, R = 8 * NB, kThreads = 32 * WARPS;
     constexpr int KW = D / 32;                     // K words per token and lane; V words per lane and p
@@ -411,26 +409,29 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
     __shared__ int64_t pre[kThreads + 1];          // units before each thread's sequences
     __shared__ int64_t warp_sum[WARPS];
     __shared__ Part parts[2 * WARPS];
+    __shared__ float part_w[2 * WARPS][R], part_n[2 * WARPS][R], part_l[2 * WARPS][R];
     __shared__ uint32_t abort_word;
     __shared__ int last_flag[2];
     volatile uint32_t *abort_flag = &abort_word;
     const uint32_t sbase = smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int gid = lane >> 2, tig = lane & 3;
+    auto work_of = [&](int b) {
+        return seq_work(p.cu[b], p.cu[b + 1], p.kv_lens[b], p.T, p.capacity, p.window, p.share,
+                        p.kv_heads, R);
+    };
 
     // ---- units of all sequences: every CTA adds them up itself ----
-    const int64_t per = (p.B + kThreads - 1) / kThreads;       // sequences per thread
-    int64_t mine = 0;
-    for (int64_t i = 0; i < per; ++i) {
-        const int64_t b = tid * per + i;
+    const int per = (p.B + kThreads - 1) / kThreads;           // sequences per thread
+    int64_t scan = 0;
+    for (int i = 0; i < per; ++i) {
+        const int b = tid * per + i;
         if (b < p.B) {
-            const int64_t len = p.kv_lens[b];
+            scan += work_of(b).units;
+            const int len = p.kv_lens[b];
             if (blockIdx.x == 0 && (len < 0 || len > p.capacity)) atomicOr(p.err_word, kErrIndex);
-            mine += seq_work(p.cu[b], p.cu[b + 1], len, p.capacity, p.window, p.share, p.kv_heads,
-                             R).units;
         }
     }
-    int64_t scan = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int64_t v = __shfl_up_sync(0xFFFFFFFFu, scan, o);
@@ -439,11 +440,11 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
     if (lane == 31) warp_sum[warp] = scan;
     if (tid < 2 * WARPS) parts[tid].item_end = 0;
     if (tid == 0) abort_word = 0u;
-    if (lane == 0)
-        for (int s = 0; s < S; ++s) mbar_init(sbase + L::bars_off + 8u * (warp * S + s), 1);
-    if (tid == 0) asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    if (lane < S) mbar_init(sbase + L::bars_off + 8u * (warp * S + lane), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     __syncthreads();
     int64_t before = 0, units = 0;
+#pragma unroll
     for (int w = 0; w < WARPS; ++w) {
         if (w < warp) before += warp_sum[w];
         units += warp_sum[w];
@@ -451,100 +452,108 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
     pre[tid + 1] = before + scan;
     if (tid == 0) pre[0] = 0;
     __syncthreads();
-    const int64_t ctas = active_ctas(units, gridDim.x, p.min_units);
-    if (units == 0 || blockIdx.x >= ctas) return;
-    const int64_t cta_begin = range_begin(blockIdx.x, units, ctas);
-    const int64_t cta_end = range_begin(blockIdx.x + 1, units, ctas);
-    const int64_t w_begin = cta_begin + range_begin(warp, cta_end - cta_begin, WARPS);
-    const int64_t w_end = cta_begin + range_begin(warp + 1, cta_end - cta_begin, WARPS);
+    const int64_t quota = cta_quota(units, gridDim.x, p.min_units);
+    const int64_t cta_begin = range_begin(blockIdx.x, quota, units);
+    const int64_t cta_end = range_begin(blockIdx.x + 1, quota, units);
+    if (cta_begin >= cta_end) return;
+    const int wq = warp_quota(cta_end - cta_begin, WARPS);
+    const int64_t w_begin = min(cta_begin + (int64_t)warp * wq, cta_end);
+    const int64_t w_end = min(w_begin + wq, cta_end);
 
     const uint32_t ring = sbase + L::ring_off + (uint32_t)warp * L::ring;
     const uint32_t bar0 = sbase + L::bars_off + 8u * (uint32_t)(warp * S);
     int stage = 0;                                 // next stage to consume
     uint32_t phase = 0;
     bool ok = true;
-    int in_flight = 0;                             // copies to wait for after a failed wait
+    int in_flight = 0;                             // stages to wait for after a failed wait
 
     if (w_begin < w_end) {
-        // the sequence that holds unit w_begin
+        // the sequence that holds unit w_begin: the last thread whose prefix is
+        // not above it has units (threads without share the next one's prefix)
         int lo = 0;
         for (int i = lane; i < kThreads; i += 32)
             if (pre[i] <= w_begin) lo = i;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) lo = max(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
-        // (threads without units share their prefix with the next one, so the
-        // last thread at or below w_begin has units)
-        int64_t b = lo * per, seq_begin = pre[lo];
+        lo = __reduce_max_sync(0xFFFFFFFFu, lo);
+        int b = lo * per;
+        int64_t seq_begin = pre[lo];
         SeqWork sw;
         for (;; ++b) {
-            sw = seq_work(p.cu[b], p.cu[b + 1], p.kv_lens[b], p.capacity, p.window, p.share,
-                          p.kv_heads, R);
+            sw = work_of(b);
             if (w_begin < seq_begin + sw.units) break;
             seq_begin += sw.units;
         }
         int64_t u = w_begin;
-        int64_t item = (u - seq_begin) / sw.blocks;            // (head, row tile) of the sequence
-        while (u < w_end && ok) {
+        int item = (int)((u - seq_begin) / sw.blocks);         // (head, row tile) of the sequence
+        while (u < w_end) {
             while (u >= seq_begin + sw.units) {                // next sequence with units
                 seq_begin += sw.units;
-                ++b;
-                sw = seq_work(p.cu[b], p.cu[b + 1], p.kv_lens[b], p.capacity, p.window, p.share,
-                              p.kv_heads, R);
+                sw = work_of(++b);
                 item = 0;
             }
-            const int h = (int)(item / sw.row_tiles), rt = (int)(item - h * sw.row_tiles);
-            const int64_t item_begin = seq_begin + item * sw.blocks;
+            const int h = item / sw.row_tiles, rt = item - h * sw.row_tiles;
+            const int64_t item_begin = seq_begin + (int64_t)item * sw.blocks;
             const int64_t item_end = item_begin + sw.blocks;
-            const int64_t seg_end = item_end < w_end ? item_end : w_end;
-            const int64_t blk0 = sw.block0 + (u - item_begin);
+            const int64_t seg_end = min(item_end, w_end);
+            const int blk0 = sw.block0 + (int)(u - item_begin);
             const int nblk = (int)(seg_end - u);
-            const int64_t cu0 = p.cu[b];
-            const int32_t *table = p.page_table + b * p.max_pages;
+            const int steps = (nblk + 1) >> 1;                 // two blocks each
+            const int cu0 = p.cu[b];
+            const int32_t *table = p.page_table + (int64_t)b * p.max_pages;
 
-            // ---- copies: record of block i goes to stage (stage + i) % S ----
-            int64_t rec_cur = 0;                   // lane i: record of block 32 * chunk + i
-            uint32_t bad = 0;                      // stages whose block has no page
-            const int stage0 = stage;
-            auto load_chunk = [&](int first) {
-                const int i = first + lane;
-                rec_cur = -1;
-                if (i < nblk && (blk0 + i) * kBlock < sw.len)
-                    rec_cur = record_index(table, p.max_pages, p.num_pages, p.kv_heads, h,
-                                           p.page_blocks, blk0 + i);
+            // ---- copies: step i's records go to stage (stage0 + i) % S ----
+            // lane l holds the place of block 32 c + l of the segment, and of
+            // block 32 (c + 1) + l
+            const uint8_t *src_cur, *src_next;
+            auto place = [&](int i) -> const uint8_t * {
+                if (i >= nblk || (blk0 + i) * kBlock >= sw.len) return nullptr;
+                const int64_t r = record_index(table, p.max_pages, p.num_pages, p.kv_heads, h,
+                                               p.page_blocks, blk0 + i);
+                return r < 0 ? nullptr : p.cache + r * L::rec;
             };
-            auto issue = [&](int i) {              // block i of the segment
-                if ((i & 31) == 0) load_chunk(i);
-                const int64_t rec = __shfl_sync(0xFFFFFFFFu, rec_cur, i & 31);
+            src_next = place(lane);
+            uint32_t have = 0;                     // two bits per stage: its records exist
+            const int stage0 = stage;
+            auto issue = [&](int i) {
+                if ((i & 15) == 0) {
+                    src_cur = src_next;
+                    src_next = place(2 * i + 32 + lane);
+                }
+                const uint8_t *src = reinterpret_cast<const uint8_t *>(__shfl_sync(
+                    0xFFFFFFFFu, reinterpret_cast<unsigned long long>(src_cur), ((2 * i) & 31) + (lane & 1)));
+                const uint32_t got = __ballot_sync(0xFFFFFFFFu, src != nullptr) & 3u;
                 int s = stage0 + i % S;
                 if (s >= S) s -= S;
-                bad = rec < 0 ? bad | (1u << s) : bad & ~(1u << s);
-                if (lane == 0) {
-                    if (rec < 0) {
-                        mbar_arrive(bar0 + 8u * s);
-                    } else {
-                        mbar_arrive_expect_tx(bar0 + 8u * s, (uint32_t)L::rec);
-                        bulk_copy(ring + (uint32_t)s * L::rec, p.cache + rec * L::rec,
-                                  (uint32_t)L::rec, bar0 + 8u * s);
-                    }
-                }
+                have = (have & ~(3u << (2 * s))) | got << (2 * s);
+                const uint32_t bar = bar0 + 8u * s;
+                if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)L::rec * __popc(got));
+                __syncwarp();
+                if (lane < 2 && src != nullptr)
+                    bulk_copy(ring + (uint32_t)(2 * s + lane) * L::rec, src, (uint32_t)L::rec, bar);
             };
-            for (int i = 0; i < S && i < nblk; ++i) issue(i);
+            for (int i = 0; i < S && i < steps; ++i) issue(i);
 
             // ---- queries: B fragments, row gid of each 8-row tile ----
-            uint32_t qf[NB][4 * KW];
+            uint32_t qf[L::q_smem ? 1 : NB][L::q_smem ? 1 : 4 * KW];
+            const uint32_t q_area = sbase + L::q_off + (uint32_t)warp * L::q_bytes + 16u * lane;
             float kq[NB][2];                       // per column 2 tig, 2 tig + 1
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
-                const int64_t r = (int64_t)rt * R + 8 * nb + gid;
-                const int64_t tok = row_token(r, sw.n, p.share, cu0, p.T);
+                const int r = rt * R + 8 * nb + gid;
+                const uint16_t *src = nullptr;
+                if (r < sw.n * p.share) {
+                    const int i = r / p.share, tok = cu0 + i;
+                    if (tok < p.T)
+                        src = p.q + (int64_t)tok * p.q_stride +
+                              (int64_t)(h * p.share + r - i * p.share) * D + 8 * tig;
+                }
                 uint4 x[KW];
-                const uint16_t *src =
-                    p.q + tok * p.q_stride + ((int64_t)h * p.share + r % p.share) * D + 8 * tig;
                 float big = 0.0f;
 #pragma unroll
+                for (int j = 0; j < KW; ++j)
+                    x[j] = src ? *reinterpret_cast<const uint4 *>(src + 32 * j)
+                               : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
                 for (int j = 0; j < KW; ++j) {
-                    x[j] = tok >= 0 ? *reinterpret_cast<const uint4 *>(src + 32 * j)
-                                    : make_uint4(0u, 0u, 0u, 0u);
                     const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
@@ -566,37 +575,38 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                         v[2 * i + 1] = dev::bf16_hi(w[i]) * f;
                     }
                     // a word's code pairs: nibbles (0,4), (1,5), (2,6), (3,7)
+                    uint32_t f4[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) qf[nb][4 * j + i] = pack_f16x2(v[i], v[i + 4]);
+                    for (int i = 0; i < 4; ++i) f4[i] = pack_f16x2(v[i], v[i + 4]);
+                    if constexpr (L::q_smem) {
+                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
+                                         q_area + 512u * (uint32_t)(j * NB + nb)),
+                                     "r"(f4[0]), "r"(f4[1]), "r"(f4[2]), "r"(f4[3]) : "memory");
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) qf[nb][4 * j + i] = f4[i];
+                    }
                 }
                 const float kr = p.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23);
                 kq[nb][0] = __shfl_sync(0xFFFFFFFFu, kr, 8 * tig);
                 kq[nb][1] = __shfl_sync(0xFFFFFFFFu, kr, 8 * tig + 4);
             }
             // keys each column's row may see: [klo, khi)
-            int64_t khi[NB][2], klo[NB][2];
-            int64_t all_hi = sw.len, all_lo = 0, any_hi = 0;
-            {
-                const int64_t pos0 = sw.len - sw.n;
-                const int64_t r0 = (int64_t)rt * R;
-                int64_t r1 = r0 + R - 1;
-                if (r1 > sw.n * p.share - 1) r1 = sw.n * p.share - 1;
-                all_hi = pos0 + r0 / p.share + 1;
-                any_hi = pos0 + r1 / p.share + 1;
-                all_lo = p.window > 0 ? any_hi - p.window : 0;
+            int khi[NB][2], klo[NB][2];
+            const int pos0 = sw.len - sw.n;
+            const int r0 = rt * R, r1 = min(r0 + R, sw.n * p.share) - 1;
+            const int all_hi = pos0 + r0 / p.share + 1, any_hi = pos0 + r1 / p.share + 1;
+            const int all_lo = p.window > 0 ? max(any_hi, 0) - p.window : 0;
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
+            for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        int64_t r = r0 + 8 * nb + 2 * tig + c;
-                        if (r > r1) r = r1;
-                        khi[nb][c] = pos0 + r / p.share + 1;
-                        klo[nb][c] = p.window > 0 ? khi[nb][c] - p.window : 0;
-                    }
-            }
+                for (int c = 0; c < 2; ++c) {
+                    khi[nb][c] = pos0 + min(r0 + 8 * nb + 2 * tig + c, r1) / p.share + 1;
+                    klo[nb][c] = p.window > 0 ? max(khi[nb][c], 0) - p.window : 0;
+                }
 
             // ---- main loop ----
-            float acc[4 * VW][NB][4], l[NB][2], m[NB][2], nm[NB][2], cf[NB][2];
+            float acc[4 * VW][NB][4], l[NB][2], nm[NB][2];
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -606,26 +616,30 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     l[nb][c] = 0.0f;
-                    m[nb][c] = nm[nb][c] = kNoMax;
-                    cf[nb][c] = 1.0f;
+                    nm[nb][c] = kNoMax;
                 }
             }
-            for (int i = 0; i < nblk; ++i) {
-                ok = mbar_wait(bar0 + 8u * stage, phase, p.wait_limit, abort_flag, p.err_word);
+            for (int i = 0; i < steps; ++i) {
+                ok = ring_wait(bar0 + 8u * stage, phase, p.wait_limit, abort_flag, p.err_word);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) {
-                    in_flight = min(S, nblk - i);
+                    in_flight = min(S, steps - i);
                     break;
                 }
-                const uint32_t st = ring + (uint32_t)stage * L::rec;
-                const int64_t key0 = (blk0 + i) * kBlock;
-                if (key0 < any_hi) {
-                    if ((bad >> stage) & 1u) {
-                        // a block of existing keys without a page
-                        if (lane == 0 && key0 < sw.len) atomicOr(p.err_word, kErrIndex);
-                    } else {
-                        // -- scores: tokens gid and gid + 8, columns 2 tig, 2 tig + 1
-                        float s[NB][4];
+                const int key0 = (blk0 + 2 * i) * kBlock;
+                const uint32_t got = (have >> (2 * stage)) & 3u;
+                if (key0 < any_hi && got != 0) {
+                    // a record that was not copied holds an earlier one's bytes
+                    // (or none yet): all its keys are masked
+                    const uint32_t st0 = ring + (uint32_t)(2 * stage) * L::rec;
+                    const uint32_t st1 = got == 3u ? st0 + L::rec : got == 1u ? st0 : st0 + L::rec;
+                    const uint32_t sr[2] = {got == 2u ? st1 : st0, st1};
+                    float s[2][NB][4], vs[2][NG][2], vl[2][2];
+                    // -- scores (without kq): tokens gid and gid + 8 of each
+                    //    record, columns 2 tig, 2 tig + 1
+#pragma unroll
+                    for (int rc = 0; rc < 2; ++rc) {
+                        const uint32_t st = sr[rc];
                         uint32_t kw[2][KW];
 #pragma unroll
                         for (int q = 0; q < (2 * KW + 3) / 4; ++q) {
@@ -634,10 +648,6 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
 #pragma unroll
                             for (int x = 0; x < 4; ++x) kw[(4 * q + x) / KW][(4 * q + x) % KW] = t[x];
                         }
-#pragma unroll
-                        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) s[nb][c] = 0.0f;
 #pragma unroll
                         for (int gr = 0; gr < NG; ++gr) {
                             float t[NB][4];
@@ -649,21 +659,31 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
 #pragma unroll
                             for (int x = 0; x < 2; ++x) {
                                 const uint32_t z = lds_u8(st + k_zeros_off(D, NG) + 16u * gr + gid + 8 * x);
-                                z1[x] = (0x6400u + z) * 0x00010001u;
-                                z2[x] = (0x5400u + 16u * z) * 0x00010001u;
+                                z1[x] = z * 0x00010001u + 0x64006400u;
+                                z2[x] = z * 0x00100010u + 0x54005400u;
                             }
 #pragma unroll
                             for (int jj = 0; jj < G / 32; ++jj) {
                                 const int j = gr * (G / 32) + jj;
+                                uint4 qv[L::q_smem ? NB : 1];
+                                if constexpr (L::q_smem)
+#pragma unroll
+                                    for (int nb = 0; nb < NB; ++nb)
+                                        qv[nb] = lds128(q_area + 512u * (uint32_t)(j * NB + nb));
 #pragma unroll
                                 for (int half = 0; half < 2; ++half) {
                                     const uint32_t a = kw[0][j] >> (8 * half), c = kw[1][j] >> (8 * half);
                                     const uint32_t a0 = codes_lo(a, z1[0]), a1 = codes_lo(c, z1[1]);
                                     const uint32_t a2 = codes_hi(a, z2[0]), a3 = codes_hi(c, z2[1]);
 #pragma unroll
-                                    for (int nb = 0; nb < NB; ++nb)
-                                        mma_f16(t[nb], a0, a1, a2, a3, qf[nb][4 * j + 2 * half],
-                                                qf[nb][4 * j + 2 * half + 1]);
+                                    for (int nb = 0; nb < NB; ++nb) {
+                                        if constexpr (L::q_smem)
+                                            mma_f16(t[nb], a0, a1, a2, a3, half ? qv[nb].z : qv[nb].x,
+                                                    half ? qv[nb].w : qv[nb].y);
+                                        else
+                                            mma_f16(t[nb], a0, a1, a2, a3, qf[nb][4 * j + 2 * half],
+                                                    qf[nb][4 * j + 2 * half + 1]);
+                                    }
                                 }
                             }
 #pragma unroll
@@ -674,97 +694,104 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                                     for (int c = 0; c < 2; ++c)
-                                        s[nb][2 * x + c] = fmaf(t[nb][2 * x + c], sc, s[nb][2 * x + c]);
+                                        s[rc][nb][2 * x + c] =
+                                            gr == 0 ? t[nb][2 * x + c] * sc
+                                                    : fmaf(t[nb][2 * x + c], sc, s[rc][nb][2 * x + c]);
                             }
                         }
+                        // -- V scales, log2 of the largest
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            float top = 0.0f;
+#pragma unroll
+                            for (int gr = 0; gr < NG; ++gr) {
+                                vs[rc][gr][x] = __uint_as_float(
+                                    lds_u16(st + v_scales_off(D, NG) + 32u * gr + 2u * (gid + 8 * x)) << 16);
+                                top = fmaxf(top, vs[rc][gr][x]);
+                            }
+                            vl[rc][x] = fminf(fmaxf(lg2(top), -100.0f), 100.0f);
+                        }
+                    }
+                    // -- scores in powers of two, masks
+#pragma unroll
+                    for (int rc = 0; rc < 2; ++rc)
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) s[nb][c] *= kq[nb][c & 1];
-                        // -- V scales; binade of the largest
-                        float vs[NG][2], ve[2];
+                            for (int c = 0; c < 4; ++c) s[rc][nb][c] *= kq[nb][c & 1];
+                    if (got != 3u || key0 < all_lo || key0 + 2 * kBlock > all_hi) {
+                        if (lane == 0)
+                            for (int rc = 0; rc < 2; ++rc)      // existing keys without a page
+                                if (!((got >> rc) & 1u) && 2 * i + rc < nblk && key0 + 16 * rc < sw.len)
+                                    atomicOr(p.err_word, kErrIndex);
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            uint32_t top = 0;
-#pragma unroll
-                            for (int gr = 0; gr < NG; ++gr) {
-                                const uint32_t bits = lds_u16(st + v_scales_off(D, NG) + 32u * gr + 2u * (gid + 8 * x));
-                                vs[gr][x] = __uint_as_float(bits << 16);
-                                top = max(top, bits);
-                            }
-                            ve[x] = (float)((int)max(top >> 7, 1u) - 126);     // S < 2^ve
-                        }
-                        // -- masks
-                        if (key0 < all_lo || key0 + kBlock > all_hi) {
+                        for (int rc = 0; rc < 2; ++rc)
 #pragma unroll
                             for (int x = 0; x < 2; ++x) {
-                                const int64_t key = key0 + gid + 8 * x;
-                                if (key >= sw.len) {       // never written: whatever it holds
+                                const int key = key0 + 16 * rc + gid + 8 * x;
+                                const bool none = !((got >> rc) & 1u) || key >= sw.len;
+                                if (none) {                     // not written: whatever it holds
+                                    vl[rc][x] = 0.0f;
 #pragma unroll
-                                    for (int gr = 0; gr < NG; ++gr) vs[gr][x] = 0.0f;
+                                    for (int gr = 0; gr < NG; ++gr) vs[rc][gr][x] = 0.0f;
                                 }
 #pragma unroll
                                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                                     for (int c = 0; c < 2; ++c)
-                                        if (key >= khi[nb][c] || key < klo[nb][c])
-                                            s[nb][2 * x + c] = __int_as_float(0xFF800000);
+                                        if (none || key >= khi[nb][c] || key < klo[nb][c])
+                                            s[rc][nb][2 * x + c] = __int_as_float(0xFF800000);
                             }
-                        }
-                        // -- running maxima: raised only when a score is 2^8, or a
-                        //    weight 2^4, above them (fp16 holds weights below 2^16)
-                        bool raise = false;
+                    }
+                    // -- running maximum: raised only when a weight would be 2^4 or
+                    //    more (fp16 holds weights below 2^16)
+                    bool raise = false;
+#pragma unroll
+                    for (int rc = 0; rc < 2; ++rc)
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                             for (int c = 0; c < 4; ++c)
-                                raise |= s[nb][c] > m[nb][c & 1] + 8.0f ||
-                                         s[nb][c] + ve[c >> 1] > nm[nb][c & 1] + 4.0f;
-                        if (__any_sync(0xFFFFFFFFu, raise)) {
-#pragma unroll
-                            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                                for (int c = 0; c < 2; ++c) {
-                                    float a = fmaxf(s[nb][c], s[nb][c + 2]);
-                                    float d = fmaxf(s[nb][c] + ve[0], s[nb][c + 2] + ve[1]);
-#pragma unroll
-                                    for (int o = 4; o < 32; o <<= 1) {
-                                        a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
-                                        d = fmaxf(d, __shfl_xor_sync(0xFFFFFFFFu, d, o));
-                                    }
-                                    a = fmaxf(a, m[nb][c]);
-                                    d = fmaxf(d, nm[nb][c]);
-                                    const float fl = ex2(m[nb][c] - a), fo = ex2(nm[nb][c] - d);
-                                    m[nb][c] = a;
-                                    nm[nb][c] = d;
-                                    cf[nb][c] = ex2(a - d);
-                                    l[nb][c] *= fl;
-#pragma unroll
-                                    for (int y = 0; y < 4 * VW; ++y) {
-                                        acc[y][nb][c] *= fo;
-                                        acc[y][nb][c + 2] *= fo;
-                                    }
-                                }
-                        }
-                        // -- weights
+                                raise |= s[rc][nb][c] + vl[rc][c >> 1] > nm[nb][c & 1] + 4.0f;
+                    if (__any_sync(0xFFFFFFFFu, raise)) {
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                s[nb][c] = ex2(s[nb][c] - m[nb][c & 1]);
-                                l[nb][c & 1] += s[nb][c];
-                                s[nb][c] *= cf[nb][c & 1];
+                            for (int c = 0; c < 2; ++c) {
+                                float d = fmaxf(fmaxf(s[0][nb][c] + vl[0][0], s[0][nb][c + 2] + vl[0][1]),
+                                                fmaxf(s[1][nb][c] + vl[1][0], s[1][nb][c + 2] + vl[1][1]));
+#pragma unroll
+                                for (int o = 4; o < 32; o <<= 1)
+                                    d = fmaxf(d, __shfl_xor_sync(0xFFFFFFFFu, d, o));
+                                d = fmaxf(d, nm[nb][c]);
+                                const float fo = ex2(nm[nb][c] - d);
+                                nm[nb][c] = d;
+                                l[nb][c] *= fo;
+#pragma unroll
+                                for (int y = 0; y < 4 * VW; ++y) {
+                                    acc[y][nb][c] *= fo;
+                                    acc[y][nb][c + 2] *= fo;
+                                }
                             }
+                    }
+                    // -- weights, values: rows d, columns 2 tig, 2 tig + 1
+#pragma unroll
+                    for (int rc = 0; rc < 2; ++rc) {
+                        const uint32_t st = sr[rc];
                         uint32_t wf[NG][NB][2];
 #pragma unroll
-                        for (int gr = 0; gr < NG; ++gr)
+                        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                            for (int nb = 0; nb < NB; ++nb)
+                            for (int x = 0; x < 2; ++x) {
+                                const float p0 = ex2(s[rc][nb][2 * x] - nm[nb][0]);
+                                const float p1 = ex2(s[rc][nb][2 * x + 1] - nm[nb][1]);
+                                l[nb][0] += p0;
+                                l[nb][1] += p1;
 #pragma unroll
-                                for (int x = 0; x < 2; ++x)
-                                    wf[gr][nb][x] = transpose8(pack_f16x2(
-                                        s[nb][2 * x] * vs[gr][x], s[nb][2 * x + 1] * vs[gr][x]));
-                        // -- values: rows d, columns 2 tig, 2 tig + 1
+                                for (int gr = 0; gr < NG; ++gr)
+                                    wf[gr][nb][x] = transpose8(
+                                        pack_f16x2(p0 * vs[rc][gr][x], p1 * vs[rc][gr][x]));
+                            }
                         uint32_t vw[2][KW];
 #pragma unroll
                         for (int q = 0; q < (2 * KW + 3) / 4; ++q) {
@@ -804,59 +831,41 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                                             wf[gr][nb][1]);
                             }
                     }
+                } else if (key0 < any_hi && lane == 0 && key0 < sw.len) {
+                    atomicOr(p.err_word, kErrIndex);           // neither record has a page
                 }
                 // every register loaded from the stage has been consumed by an
                 // MMA or a conversion: it may be filled again
                 __syncwarp();
                 if (++stage == S) { stage = 0; phase ^= 1u; }
-                if (i + S < nblk) issue(i + S);
+                if (i + S < steps) issue(i + S);
             }
             if (!ok) break;
 
             // ---- the segment's result ----
             const bool whole = u == item_begin && seg_end == item_end;
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float t = l[nb][c];
-#pragma unroll
-                    for (int o = 4; o < 32; o <<= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
-                    l[nb][c] = t;
-                }
             float *slot = nullptr;
             if (!whole) {
-                // the last segment's goes over the idle ring, an earlier one's
-                // into the warp's own slot
+                // the last segment's part goes over the idle ring, an earlier
+                // one's (it began in front of this warp's range) beside it
                 const bool last = seg_end == w_end;
                 slot = reinterpret_cast<float *>(smem + (last ? L::ring_off + warp * L::ring
                                                               : L::first_off + warp * L::slot));
-                if (lane == 0) {
-                    Part &pt = parts[2 * warp + (last ? 1 : 0)];
-                    pt.item_begin = item_begin;
-                    pt.item_end = item_end;
-                    pt.b = b;
-                    pt.h = h;
-                    pt.rt = rt;
-                }
+                if (lane == 0) parts[2 * warp + (last ? 1 : 0)] = Part{item_begin, item_end, b, h, rt};
             }
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const int row = 8 * nb + 2 * tig + c;
-                    float f = 1.0f;
-                    int64_t tok = -1;
-                    uint16_t *dst = nullptr;
-                    if (whole) {
-                        const int64_t r = (int64_t)rt * R + row;
-                        tok = row_token(r, sw.n, p.share, cu0, p.T);
-                        f = row_factor(m[nb][c], nm[nb][c], l[nb][c]);
-                        dst = p.out + tok * p.out_stride + ((int64_t)h * p.share + r % p.share) * D;
-                    } else if (gid == 0) {
-                        slot[SL::stats + row] = m[nb][c];
-                        slot[SL::stats + R + row] = nm[nb][c];
-                        slot[SL::stats + 2 * R + row] = l[nb][c];
+                    float t = l[nb][c];
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+                    const float f = row_factor(t);
+                    uint16_t *dst = whole ? out_row<D>(p, cu0, sw.n, h, rt * R + row) : nullptr;
+                    if (!whole && gid == 0) {
+                        slot[SL::stats + row] = nm[nb][c];
+                        slot[SL::stats + R + row] = t;
                     }
 #pragma unroll
                     for (int wi = 0; wi < VW; ++wi)
@@ -866,11 +875,10 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                             for (int hi = 0; hi < 2; ++hi) {
                                 const int d = 64 * wi + 16 * nib + 8 * hi + gid;
                                 const float o = acc[4 * wi + nib][nb][2 * hi + c];
-                                if (whole) {
-                                    if (tok >= 0) dst[d] = (uint16_t)dev::f32_to_bf16_rne(o * f);
-                                } else {
+                                if (!whole)
                                     slot[row * SL::pitch + d] = o;
-                                }
+                                else if (dst)
+                                    dst[d] = (uint16_t)dev::f32_to_bf16_rne(o * f);
                             }
                 }
             u = seg_end;
@@ -888,77 +896,137 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
     if (*abort_flag) return;
 
     // ---- items shared by warps ----
-    Part pend[2];                                   // items shared with other CTAs, by slot
-    pend[0].item_end = pend[1].item_end = 0;
     auto slot_of = [&](int i) {                     // of parts[i]
         return reinterpret_cast<const float *>(
             smem + ((i & 1) ? L::ring_off + (i >> 1) * L::ring : L::first_off + (i >> 1) * L::slot));
     };
+    // per part and row: its factor, and the item's maximum and sum
+    for (int e = tid; e < 2 * WARPS * R; e += kThreads) {
+        const int i = e / R, row = e - i * R;
+        if (parts[i].item_end == 0) continue;
+        float n = kNoMax, l = 0.0f;
+        for (int j = 0; j < 2 * WARPS; ++j)
+            if (parts[j].item_end != 0 && parts[j].item_begin == parts[i].item_begin)
+                n = fmaxf(n, slot_of(j)[SL::stats + row]);
+        for (int j = 0; j < 2 * WARPS; ++j)
+            if (parts[j].item_end != 0 && parts[j].item_begin == parts[i].item_begin)
+                l += slot_of(j)[SL::stats + R + row] * ex2(slot_of(j)[SL::stats + row] - n);
+        part_w[i][row] = ex2(slot_of(i)[SL::stats + row] - n);
+        part_n[i][row] = n;
+        part_l[i][row] = l;
+    }
+    __syncthreads();
+    int pend0 = -1, pend1 = -1;                     // first parts of items shared with other CTAs
     for (int i = 0; i < 2 * WARPS;) {
         if (parts[i].item_end == 0) { ++i; continue; }
         const Part it = parts[i];
-        const float *list[WARPS];                   // at most one part of an item per warp
-        int count = 0;
-        for (; i < 2 * WARPS; ++i) {
-            if (parts[i].item_end == 0) continue;
-            if (parts[i].item_begin != it.item_begin) break;
-            list[count++] = slot_of(i);
-        }
-        float *dst = nullptr;
+        int j = i + 1;                              // parts i .. j - 1 are the item's
+        while (j < 2 * WARPS && (parts[j].item_end == 0 || parts[j].item_begin == it.item_begin)) ++j;
+        float *part_dst = nullptr;
         if (it.item_begin < cta_begin || it.item_end > cta_end) {
             const int sl = partial_slot(it.item_begin, cta_begin);
-            dst = p.partials + ((int64_t)blockIdx.x * 2 + sl) * SL::floats;
-            pend[sl] = it;
+            part_dst = p.partials + ((int64_t)blockIdx.x * 2 + sl) * SL::floats;
+            if (sl) pend1 = i;
+            else pend0 = i;
         }
-        merge_parts<D, NB, false>(p, [&](int x) { return list[x]; }, count, dst, it, tid, kThreads);
+        const int cu0 = p.cu[it.b], n = p.cu[it.b + 1] - cu0;
+        for (int e = tid; e < R * D / 4; e += kThreads) {
+            const int row = e / (D / 4), d = 4 * (e - row * (D / 4));
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int x = i; x < j; ++x) {
+                if (parts[x].item_end == 0) continue;
+                const float4 v = *reinterpret_cast<const float4 *>(slot_of(x) + row * SL::pitch + d);
+                const float w = part_w[x][row];
+                o.x += w * v.x; o.y += w * v.y; o.z += w * v.z; o.w += w * v.w;
+            }
+            if (part_dst) {
+                __stcg(reinterpret_cast<float4 *>(part_dst + row * SL::pitch + d), o);
+                if (d == 0) {
+                    __stcg(part_dst + SL::stats + row, part_n[i][row]);
+                    __stcg(part_dst + SL::stats + R + row, part_l[i][row]);
+                }
+            } else if (uint16_t *dst = out_row<D>(p, cu0, n, it.h, it.rt * R + row)) {
+                store4(dst + d, o, row_factor(part_l[i][row]));
+            }
+        }
+        i = j;
     }
-    if (pend[0].item_end == 0 && pend[1].item_end == 0) return;
+    if (pend0 < 0 && pend1 < 0) return;
     // ---- items shared by CTAs: the last to arrive adds the parts in order ----
     __threadfence();
     __syncthreads();
-    if (tid == 0) {
-        for (int sl = 0; sl < 2; ++sl) {
-            last_flag[sl] = 0;
-            if (pend[sl].item_end == 0) continue;
-            const int64_t c0 = worker_of(pend[sl].item_begin, units, ctas);
-            const int64_t c1 = worker_of(pend[sl].item_end - 1, units, ctas);
-            last_flag[sl] = atomicAdd(&p.counters[c0], 1u) == (uint32_t)(c1 - c0);
+    if (tid < 2) {
+        const int pi = tid ? pend1 : pend0;
+        last_flag[tid] = 0;
+        if (pi >= 0) {
+            const int64_t c0 = parts[pi].item_begin / quota, c1 = (parts[pi].item_end - 1) / quota;
+            last_flag[tid] = atomicAdd(&p.counters[c0], 1u) == (uint32_t)(c1 - c0);
         }
     }
     __syncthreads();
+    float *factors = reinterpret_cast<float *>(smem);       // [parts][R]; the rings are idle
     for (int sl = 0; sl < 2; ++sl) {
         if (!last_flag[sl]) continue;
         __threadfence();
-        const Part it = pend[sl];
-        const int64_t c0 = worker_of(it.item_begin, units, ctas);
-        const int64_t c1 = worker_of(it.item_end - 1, units, ctas);
-        const int s0 = partial_slot(it.item_begin, range_begin(c0, units, ctas));
+        const Part it = parts[sl ? pend1 : pend0];
+        const int64_t c0 = it.item_begin / quota;
+        const int count = (int)((it.item_end - 1) / quota - c0) + 1;
+        const int s0 = partial_slot(it.item_begin, range_begin(c0, quota, units));
         const float *base = p.partials + 2 * c0 * SL::floats;
-        merge_parts<D, NB, true>(
-            p, [&](int x) { return base + ((int64_t)2 * x + (x == 0 ? s0 : 0)) * SL::floats; },
-            (int)(c1 - c0 + 1), nullptr, it, tid, kThreads);
+        auto part = [&](int x) { return base + (int64_t)(2 * x + (x == 0 ? s0 : 0)) * SL::floats; };
+        for (int row = warp; row < R; row += WARPS) {
+            float n = kNoMax, l = 0.0f;
+            for (int x = lane; x < count; x += 32) n = fmaxf(n, __ldcg(part(x) + SL::stats + row));
+#pragma unroll
+            for (int o = 16; o; o >>= 1) n = fmaxf(n, __shfl_xor_sync(0xFFFFFFFFu, n, o));
+            for (int x = lane; x < count; x += 32) {
+                const float w = ex2(__ldcg(part(x) + SL::stats + row) - n);
+                factors[x * R + row] = w;
+                l += __ldcg(part(x) + SL::stats + R + row) * w;
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+            if (lane == 0) part_l[0][row] = l;
+        }
+        __syncthreads();
+        const int cu0 = p.cu[it.b], n = p.cu[it.b + 1] - cu0;
+        for (int e = tid; e < R * D / 4; e += kThreads) {
+            const int row = e / (D / 4), d = 4 * (e - row * (D / 4));
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+            for (int x = 0; x < count; ++x) {
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(part(x) + row * SL::pitch + d));
+                const float w = factors[x * R + row];
+                o.x += w * v.x; o.y += w * v.y; o.z += w * v.z; o.w += w * v.w;
+            }
+            if (uint16_t *dst = out_row<D>(p, cu0, n, it.h, it.rt * R + row))
+                store4(dst + d, o, row_factor(part_l[0][row]));
+        }
         if (tid == 0) p.counters[c0] = 0u;
+        __syncthreads();
     }
 }
 
 // ---------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------
-// CTAs share an SM two by two; warps per CTA so that the accumulators and
-// queries of NB 8-row tiles stay in registers.
+// CTAs per SM, and warps per CTA so that the accumulators and queries of NB
+// 8-row tiles stay in registers (and the rings of 4 groups in shared memory).
+constexpr int kAttnCtasPerSm = 2;      // at most
 template <int D, int NB>
-constexpr int kAttnWarps = D == 256 ? (NB == 1 ? 4 : 3) : (NB == 1 ? 8 : 6);
-constexpr int kAttnCtasPerSm = 2;
+constexpr int kAttnCtas = D == 256 && NB == 2 ? 1 : kAttnCtasPerSm;
+template <int D, int G, int NB>
+constexpr int kAttnWarps = D == 256 ? (NB == 1 ? 4 : 5) : NB == 2 ? 6 : D / G == 4 ? 7 : 8;
 
 // Rows of a tile: 8 when a sequence has at most 8 rows per key head on
 // average, else 16 (the keys are read once per tile).
 int attn_tiles(int64_t T, int64_t B, int64_t share) { return T * share <= 8 * B ? 1 : 2; }
 
 template <int D, int G, int NB>
-qz_status launch_attn(const AttnArgs &args, int64_t ctas, cudaStream_t st) {
-    constexpr int W = kAttnWarps<D, NB>;
-    using L = AttnLayout<D, G, NB, W>;
-    auto kernel = kv4_attention_kernel<D, G, NB, W, kAttnCtasPerSm>;
+qz_status launch_attn(const AttnArgs &args, cudaStream_t st) {
+    constexpr int W = kAttnWarps<D, G, NB>, C = kAttnCtas<D, NB>;
+    using L = AttnLayout<D, G, NB, W, C>;
+    auto kernel = kv4_attention_kernel<D, G, NB, W, C>;
     static DeviceOnce attr_once;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) {
@@ -973,7 +1041,7 @@ qz_status launch_attn(const AttnArgs &args, int64_t ctas, cudaStream_t st) {
             return e;
         }) != cudaSuccess)
         return QZ_ERR_CUDA;
-    kernel<<<(unsigned)ctas, 32 * W, L::bytes, st>>>(args);
+    kernel<<<(unsigned)(device_sm_count() * C), 32 * W, L::bytes, st>>>(args);
     return launch_status();
 }
 
@@ -1002,8 +1070,8 @@ struct Read {
 };
 template <int D, int G>
 struct Attend {
-    static qz_status go(const AttnArgs &p, int tiles, int64_t ctas, cudaStream_t st) {
-        return tiles == 1 ? launch_attn<D, G, 1>(p, ctas, st) : launch_attn<D, G, 2>(p, ctas, st);
+    static qz_status go(const AttnArgs &p, int tiles, cudaStream_t st) {
+        return tiles == 1 ? launch_attn<D, G, 1>(p, st) : launch_attn<D, G, 2>(p, st);
     }
 };
 
@@ -1020,7 +1088,7 @@ StoreArgs store_args(const Kv4Cache &c) {
     return p;
 }
 
-size_t slot_bytes(int64_t D, int tiles) { return (size_t)(8 * tiles * (D + 4) + 32 * tiles) * 4; }
+size_t slot_bytes(int64_t D, int tiles) { return (size_t)(8 * tiles * (D + 4) + 16 * tiles) * 4; }
 
 }  // namespace
 
@@ -1065,10 +1133,11 @@ qz_status launch_kv4_attention(const Kv4Cache &c, const void *q, int64_t q_strid
     p.page_table = static_cast<const int32_t *>(c.page_table);
     p.kv_lens = static_cast<const int32_t *>(c.kv_lens);
     p.cu = static_cast<const int32_t *>(c.cu);
-    p.T = c.T; p.B = c.B;
+    p.T = (int)c.T; p.B = (int)c.B;
     p.max_pages = c.max_pages; p.num_pages = c.num_pages;
-    p.window = window;
-    p.capacity = c.max_pages * c.page_size;
+    constexpr int64_t kMaxLen = (int64_t(1) << 31) - 32;
+    p.capacity = (int)(c.max_pages * c.page_size < kMaxLen ? c.max_pages * c.page_size : kMaxLen);
+    p.window = window < p.capacity ? (int)window : 0;      // reaches every key: none
     p.kv_heads = (int)c.kv_heads;
     p.share = (int)(q_heads / c.kv_heads);
     p.page_blocks = (int)(c.page_size / kBlock);
@@ -1076,7 +1145,6 @@ qz_status launch_kv4_attention(const Kv4Cache &c, const void *q, int64_t q_strid
     p.out = static_cast<uint16_t *>(out);
     p.out_stride = out_stride;
     const int tiles = attn_tiles(c.T, c.B, p.share);
-    const int64_t ctas = (int64_t)device_sm_count() * kAttnCtasPerSm;
     // counters first: their place does not depend on the tile size
     p.counters = static_cast<uint32_t *>(workspace);
     p.partials = reinterpret_cast<float *>(static_cast<char *>(workspace) + kCounterBytes);
@@ -1084,7 +1152,7 @@ qz_status launch_kv4_attention(const Kv4Cache &c, const void *q, int64_t q_strid
     p.wait_limit = device_wait_limit();
     p.err_word = device_error_word();
     if (p.err_word == nullptr) return QZ_ERR_CUDA;
-    return dispatch<Attend>(c.head_dim, c.group_size, p, tiles, ctas, st);
+    return dispatch<Attend>(c.head_dim, c.group_size, p, tiles, st);
 }
 
 }  // namespace qz

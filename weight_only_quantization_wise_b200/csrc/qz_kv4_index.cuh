@@ -94,43 +94,42 @@ QZ_HD int64_t find_sequence(const int32_t *cu, int64_t B, int64_t t) {
 // the sequence's rows may see.  Every item has at least one unit, so that
 // rows without keys are written too.
 struct SeqWork {
-    int64_t n, len;       // queries, keys
-    int64_t block0;       // first block of keys
-    int64_t blocks;       // units of an item (>= 1)
-    int64_t row_tiles;    // row tiles per key head
+    int n, len;           // queries, keys
+    int block0;           // first block of keys
+    int blocks;           // units of an item (>= 1)
+    int row_tiles;        // row tiles per key head
     int64_t units;        // kv_heads * row_tiles * blocks (0 when n == 0)
 };
 
-QZ_HD SeqWork seq_work(int64_t cu0, int64_t cu1, int64_t kv_len, int64_t capacity, int64_t window,
-                       int64_t share, int64_t kv_heads, int64_t tile_rows) {
+// rows: the call's token rows (rows * share < 2^31); capacity < 2^31 - 16.
+QZ_HD SeqWork seq_work(int cu0, int cu1, int kv_len, int rows, int capacity, int window, int share,
+                       int kv_heads, int tile_rows) {
     SeqWork s;
-    s.n = cu1 > cu0 ? cu1 - cu0 : 0;
+    s.n = cu0 >= 0 && cu1 > cu0 ? cu1 - cu0 : 0;
+    if (s.n > rows) s.n = rows;
     s.len = kv_len < 0 ? 0 : (kv_len > capacity ? capacity : kv_len);
-    int64_t first = window > 0 ? s.len - s.n - window + 1 : 0;
-    if (first < 0) first = 0;
-    s.block0 = first / kBlock;
-    const int64_t end = (s.len + kBlock - 1) / kBlock;
+    const int64_t first = window > 0 ? (int64_t)s.len - s.n - window + 1 : 0;
+    s.block0 = first > 0 ? (int)(first / kBlock) : 0;
+    const int end = (int)(((int64_t)s.len + kBlock - 1) / kBlock);
     s.blocks = end - s.block0 > 1 ? end - s.block0 : 1;
-    s.row_tiles = (s.n * share + tile_rows - 1) / tile_rows;
-    s.units = s.row_tiles * kv_heads * s.blocks;
+    s.row_tiles = (int)(((int64_t)s.n * share + tile_rows - 1) / tile_rows);
+    s.units = (int64_t)s.row_tiles * kv_heads * s.blocks;
     return s;
 }
 
 // The units of all items, in (sequence, head, row tile, block) order, are cut
-// into equal contiguous ranges, one per worker.
-QZ_HD int64_t range_begin(int64_t c, int64_t units, int64_t workers) {
-    return c * units / workers;
+// into contiguous ranges of `quota` units, one per CTA (the last may be
+// shorter): as many CTAs as there are, but none with fewer than min_units.
+QZ_HD int64_t cta_quota(int64_t units, int64_t ctas, int64_t min_units) {
+    const int64_t q = (units + ctas - 1) / ctas;
+    return q > min_units ? q : min_units;
 }
-// First worker whose range holds unit u.
-QZ_HD int64_t worker_of(int64_t u, int64_t units, int64_t workers) {
-    return ((u + 1) * workers - 1) / units;
+QZ_HD int64_t range_begin(int64_t c, int64_t quota, int64_t units) {
+    return c * quota < units ? c * quota : units;
 }
-// CTAs that take part: as many as there are, unless that leaves one fewer
-// than min_units units.
-QZ_HD int64_t active_ctas(int64_t units, int64_t ctas, int64_t min_units) {
-    const int64_t most = (units + min_units - 1) / min_units;
-    return most < ctas ? (most < 1 ? 1 : most) : ctas;
-}
+// Units per warp of a CTA's n units: even (two blocks make a step), so that
+// warps * warp_quota >= n.
+QZ_HD int warp_quota(int64_t n, int warps) { return (int)((n + 2 * warps - 1) / (2 * warps)) * 2; }
 // Partial results in the workspace: a CTA has two slots, 0 for an item that
 // is under way where its range begins (or begins there), 1 for one that
 // begins inside its range and goes on in the next CTA.
