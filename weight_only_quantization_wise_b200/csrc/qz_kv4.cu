@@ -291,13 +291,12 @@ struct AttnLayout {
     static constexpr int bytes = bars_off + WARPS * S * 8;
     static_assert(bytes <= attn_smem(CTAS), "the CTAs fit on an SM");
     static_assert(rec % 16 == 0 && slot % 16 == 0, "bulk copies and slots are 16-byte aligned");
-    // the last to arrive keeps a factor per part and row in the ring area
-    static_assert(WARPS * ring >= kSmCount * 2 * 8 * NB * 4, "factors of all parts fit");
+    static_assert(2 * WARPS <= 32, "a lane per part");
 };
 
 struct Part {                          // a warp's part of an item
     int64_t item_begin, item_end;      // units; item_end = 0: none
-    int b, h, rt;
+    int cu0, n, h, rt;                 // the sequence's first query row and queries; head, row tile
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -335,27 +334,13 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
 }
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
         "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-    return v;
-}
-__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=r"(v) : "r"(addr));
-    return v;
-}
-__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
-    return v;
+__device__ __forceinline__ float bf16_at(const uint8_t *q) {
+    return __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(q) << 16);
 }
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes,
                                           uint32_t bar) {
@@ -409,7 +394,6 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
     __shared__ int64_t pre[kThreads + 1];          // units before each thread's sequences
     __shared__ int64_t warp_sum[WARPS];
     __shared__ Part parts[2 * WARPS];
-    __shared__ float part_w[2 * WARPS][R], part_n[2 * WARPS][R], part_l[2 * WARPS][R];
     __shared__ uint32_t abort_word;
     __shared__ int last_flag[2];
     volatile uint32_t *abort_flag = &abort_word;
@@ -530,12 +514,8 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                 if (lane < 2 && src != nullptr)
                     bulk_copy(ring + (uint32_t)(2 * s + lane) * L::rec, src, (uint32_t)L::rec, bar);
             };
-            for (int i = 0; i < S && i < steps; ++i) issue(i);
-
-            // ---- queries: B fragments, row gid of each 8-row tile ----
-            uint32_t qf[L::q_smem ? 1 : NB][L::q_smem ? 1 : 4 * KW];
-            const uint32_t q_area = sbase + L::q_off + (uint32_t)warp * L::q_bytes + 16u * lane;
-            float kq[NB][2];                       // per column 2 tig, 2 tig + 1
+            // ---- queries: row gid of each 8-row tile ----
+            uint4 qx[NB][KW];
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
                 const int r = rt * R + 8 * nb + gid;
@@ -546,12 +526,21 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                         src = p.q + (int64_t)tok * p.q_stride +
                               (int64_t)(h * p.share + r - i * p.share) * D + 8 * tig;
                 }
-                uint4 x[KW];
-                float big = 0.0f;
 #pragma unroll
                 for (int j = 0; j < KW; ++j)
-                    x[j] = src ? *reinterpret_cast<const uint4 *>(src + 32 * j)
-                               : make_uint4(0u, 0u, 0u, 0u);
+                    qx[nb][j] = src ? __ldg(reinterpret_cast<const uint4 *>(src + 32 * j))
+                                    : make_uint4(0u, 0u, 0u, 0u);
+            }
+            for (int i = 0; i < S && i < steps; ++i) issue(i);
+
+            // ---- queries as B fragments ----
+            uint32_t qf[L::q_smem ? 1 : NB][L::q_smem ? 1 : 4 * KW];
+            const uint32_t q_area = sbase + L::q_off + (uint32_t)warp * L::q_bytes + 16u * lane;
+            float kq[NB][2];                       // per column 2 tig, 2 tig + 1
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                const uint4 (&x)[KW] = qx[nb];
+                float big = 0.0f;
 #pragma unroll
                 for (int j = 0; j < KW; ++j) {
                     const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
@@ -622,6 +611,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
             for (int i = 0; i < steps; ++i) {
                 ok = ring_wait(bar0 + 8u * stage, phase, p.wait_limit, abort_flag, p.err_word);
                 ok = __all_sync(0xFFFFFFFFu, ok);
+                
                 if (!ok) {
                     in_flight = min(S, steps - i);
                     break;
@@ -631,87 +621,100 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                 if (key0 < any_hi && got != 0) {
                     // a record that was not copied holds an earlier one's bytes
                     // (or none yet): all its keys are masked
-                    const uint32_t st0 = ring + (uint32_t)(2 * stage) * L::rec;
-                    const uint32_t st1 = got == 3u ? st0 + L::rec : got == 1u ? st0 : st0 + L::rec;
-                    const uint32_t sr[2] = {got == 2u ? st1 : st0, st1};
+                    const uint8_t *st0 = smem + L::ring_off + warp * L::ring + 2 * stage * L::rec;
+                    const uint8_t *sr[2] = {got == 2u ? st0 + L::rec : st0,
+                                            got == 1u ? st0 : st0 + L::rec};
                     float s[2][NB][4], vs[2][NG][2], vl[2][2];
                     // -- scores (without kq): tokens gid and gid + 8 of each
                     //    record, columns 2 tig, 2 tig + 1
+                    uint32_t kw[2][2][KW];
 #pragma unroll
-                    for (int rc = 0; rc < 2; ++rc) {
-                        const uint32_t st = sr[rc];
-                        uint32_t kw[2][KW];
+                    for (int rc = 0; rc < 2; ++rc)
 #pragma unroll
                         for (int q = 0; q < (2 * KW + 3) / 4; ++q) {
-                            const uint4 v = lds128(st + k_codes_off() + (uint32_t)(q * 512 + lane * 16));
+                            const uint4 v = *reinterpret_cast<const uint4 *>(
+                                sr[rc] + k_codes_off() + q * 512 + lane * 16);
                             const uint32_t t[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                            for (int x = 0; x < 4; ++x) kw[(4 * q + x) / KW][(4 * q + x) % KW] = t[x];
+                            for (int x = 0; x < 4; ++x)
+                                kw[rc][(4 * q + x) / KW][(4 * q + x) % KW] = t[x];
                         }
 #pragma unroll
-                        for (int gr = 0; gr < NG; ++gr) {
-                            float t[NB][4];
+                    for (int gr = 0; gr < NG; ++gr) {
+                        float t[2][NB][4];
+                        uint32_t z1[2][2], z2[2][2];
+#pragma unroll
+                        for (int rc = 0; rc < 2; ++rc) {
 #pragma unroll
                             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                                for (int c = 0; c < 4; ++c) t[nb][c] = 0.0f;
-                            uint32_t z1[2], z2[2];
+                                for (int c = 0; c < 4; ++c) t[rc][nb][c] = 0.0f;
 #pragma unroll
                             for (int x = 0; x < 2; ++x) {
-                                const uint32_t z = lds_u8(st + k_zeros_off(D, NG) + 16u * gr + gid + 8 * x);
-                                z1[x] = z * 0x00010001u + 0x64006400u;
-                                z2[x] = z * 0x00100010u + 0x54005400u;
+                                const uint32_t z = sr[rc][k_zeros_off(D, NG) + 16 * gr + gid + 8 * x];
+                                z1[rc][x] = z * 0x00010001u + 0x64006400u;
+                                z2[rc][x] = z * 0x00100010u + 0x54005400u;
                             }
+                        }
 #pragma unroll
-                            for (int jj = 0; jj < G / 32; ++jj) {
-                                const int j = gr * (G / 32) + jj;
-                                uint4 qv[L::q_smem ? NB : 1];
-                                if constexpr (L::q_smem)
+                        for (int jj = 0; jj < G / 32; ++jj) {
+                            const int j = gr * (G / 32) + jj;
+                            uint4 qv[L::q_smem ? NB : 1];
+                            if constexpr (L::q_smem)
 #pragma unroll
-                                    for (int nb = 0; nb < NB; ++nb)
-                                        qv[nb] = lds128(q_area + 512u * (uint32_t)(j * NB + nb));
+                                for (int nb = 0; nb < NB; ++nb)
+                                    qv[nb] = *reinterpret_cast<const uint4 *>(
+                                        smem + L::q_off + warp * L::q_bytes + 16 * lane +
+                                        512 * (j * NB + nb));
 #pragma unroll
-                                for (int half = 0; half < 2; ++half) {
-                                    const uint32_t a = kw[0][j] >> (8 * half), c = kw[1][j] >> (8 * half);
-                                    const uint32_t a0 = codes_lo(a, z1[0]), a1 = codes_lo(c, z1[1]);
-                                    const uint32_t a2 = codes_hi(a, z2[0]), a3 = codes_hi(c, z2[1]);
+                            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                                for (int rc = 0; rc < 2; ++rc) {
+                                    const uint32_t a = kw[rc][0][j] >> (8 * half);
+                                    const uint32_t c = kw[rc][1][j] >> (8 * half);
+                                    const uint32_t a0 = codes_lo(a, z1[rc][0]), a1 = codes_lo(c, z1[rc][1]);
+                                    const uint32_t a2 = codes_hi(a, z2[rc][0]), a3 = codes_hi(c, z2[rc][1]);
 #pragma unroll
                                     for (int nb = 0; nb < NB; ++nb) {
                                         if constexpr (L::q_smem)
-                                            mma_f16(t[nb], a0, a1, a2, a3, half ? qv[nb].z : qv[nb].x,
+                                            mma_f16(t[rc][nb], a0, a1, a2, a3,
+                                                    half ? qv[nb].z : qv[nb].x,
                                                     half ? qv[nb].w : qv[nb].y);
                                         else
-                                            mma_f16(t[nb], a0, a1, a2, a3, qf[nb][4 * j + 2 * half],
+                                            mma_f16(t[rc][nb], a0, a1, a2, a3,
+                                                    qf[nb][4 * j + 2 * half],
                                                     qf[nb][4 * j + 2 * half + 1]);
                                     }
                                 }
-                            }
+                        }
+#pragma unroll
+                        for (int rc = 0; rc < 2; ++rc)
 #pragma unroll
                             for (int x = 0; x < 2; ++x) {
-                                const float sc = __uint_as_float(
-                                    lds_u16(st + k_scales_off(D) + 32u * gr + 2u * (gid + 8 * x)) << 16);
+                                const float sc = bf16_at(sr[rc] + k_scales_off(D) + 32 * gr + 2 * (gid + 8 * x));
 #pragma unroll
                                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                                     for (int c = 0; c < 2; ++c)
                                         s[rc][nb][2 * x + c] =
-                                            gr == 0 ? t[nb][2 * x + c] * sc
-                                                    : fmaf(t[nb][2 * x + c], sc, s[rc][nb][2 * x + c]);
+                                            gr == 0 ? t[rc][nb][2 * x + c] * sc
+                                                    : fmaf(t[rc][nb][2 * x + c], sc, s[rc][nb][2 * x + c]);
                             }
-                        }
-                        // -- V scales, log2 of the largest
+                    }
+                    // -- V scales, log2 of the largest
+#pragma unroll
+                    for (int rc = 0; rc < 2; ++rc)
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
                             float top = 0.0f;
 #pragma unroll
                             for (int gr = 0; gr < NG; ++gr) {
-                                vs[rc][gr][x] = __uint_as_float(
-                                    lds_u16(st + v_scales_off(D, NG) + 32u * gr + 2u * (gid + 8 * x)) << 16);
+                                vs[rc][gr][x] =
+                                    bf16_at(sr[rc] + v_scales_off(D, NG) + 32 * gr + 2 * (gid + 8 * x));
                                 top = fmaxf(top, vs[rc][gr][x]);
                             }
                             vl[rc][x] = fminf(fmaxf(lg2(top), -100.0f), 100.0f);
                         }
-                    }
                     // -- scores in powers of two, masks
 #pragma unroll
                     for (int rc = 0; rc < 2; ++rc)
@@ -777,7 +780,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                     // -- weights, values: rows d, columns 2 tig, 2 tig + 1
 #pragma unroll
                     for (int rc = 0; rc < 2; ++rc) {
-                        const uint32_t st = sr[rc];
+                        const uint8_t *st = sr[rc];
                         uint32_t wf[NG][NB][2];
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb)
@@ -795,7 +798,8 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                         uint32_t vw[2][KW];
 #pragma unroll
                         for (int q = 0; q < (2 * KW + 3) / 4; ++q) {
-                            const uint4 v = lds128(st + v_codes_off(D) + (uint32_t)(q * 512 + lane * 16));
+                            const uint4 v = *reinterpret_cast<const uint4 *>(
+                                st + v_codes_off(D) + q * 512 + lane * 16);
                             const uint32_t t[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                             for (int x = 0; x < 4; ++x) vw[(4 * q + x) / KW][(4 * q + x) % KW] = t[x];
@@ -806,7 +810,8 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
 #pragma unroll
                             for (int x = 0; x < 2; ++x) {
                                 const uint32_t z = dev::prmt(
-                                    lds_u16(st + v_zeros_off(D, NG) + 16u * gr + 8u * x + 2u * tig), 0u, 0x4140u);
+                                    *reinterpret_cast<const uint16_t *>(st + v_zeros_off(D, NG) + 16 * gr + 8 * x + 2 * tig),
+                                    0u, 0x4140u);
                                 z1[gr][x] = z + 0x64006400u;
                                 z2[gr][x] = 16u * z + 0x54005400u;
                             }
@@ -842,17 +847,13 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
             }
             if (!ok) break;
 
-            // ---- the segment's result ----
+            // ---- the segment's result: rows of sums, in this warp's idle ring, or
+            // beside it when the item began in front of this warp's range and
+            // ends inside it (the ring goes on to serve)
             const bool whole = u == item_begin && seg_end == item_end;
-            float *slot = nullptr;
-            if (!whole) {
-                // the last segment's part goes over the idle ring, an earlier
-                // one's (it began in front of this warp's range) beside it
-                const bool last = seg_end == w_end;
-                slot = reinterpret_cast<float *>(smem + (last ? L::ring_off + warp * L::ring
-                                                              : L::first_off + warp * L::slot));
-                if (lane == 0) parts[2 * warp + (last ? 1 : 0)] = Part{item_begin, item_end, b, h, rt};
-            }
+            const int which = whole || seg_end == w_end ? 1 : 0;
+            float *slot = reinterpret_cast<float *>(
+                smem + (which ? L::ring_off + warp * L::ring : L::first_off + warp * L::slot));
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -861,9 +862,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                     float t = l[nb][c];
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
-                    const float f = row_factor(t);
-                    uint16_t *dst = whole ? out_row<D>(p, cu0, sw.n, h, rt * R + row) : nullptr;
-                    if (!whole && gid == 0) {
+                    if (gid == 0) {
                         slot[SL::stats + row] = nm[nb][c];
                         slot[SL::stats + R + row] = t;
                     }
@@ -872,15 +871,24 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
 #pragma unroll
                         for (int nib = 0; nib < 4; ++nib)
 #pragma unroll
-                            for (int hi = 0; hi < 2; ++hi) {
-                                const int d = 64 * wi + 16 * nib + 8 * hi + gid;
-                                const float o = acc[4 * wi + nib][nb][2 * hi + c];
-                                if (!whole)
-                                    slot[row * SL::pitch + d] = o;
-                                else if (dst)
-                                    dst[d] = (uint16_t)dev::f32_to_bf16_rne(o * f);
-                            }
+                            for (int hi = 0; hi < 2; ++hi)
+                                slot[row * SL::pitch + 64 * wi + 16 * nib + 8 * hi + gid] =
+                                    acc[4 * wi + nib][nb][2 * hi + c];
                 }
+            if (whole) {
+                __syncwarp();
+                for (int e = lane; e < R * D / 4; e += 32) {
+                    const int row = e / (D / 4), d = 4 * (e % (D / 4));
+                    if (uint16_t *dst = out_row<D>(p, cu0, sw.n, h, rt * R + row))
+                        store4(dst + d, *reinterpret_cast<const float4 *>(slot + row * SL::pitch + d),
+                               row_factor(slot[SL::stats + R + row]));
+                }
+                // the ring's next copies come behind these accesses
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+            } else if (lane == 0) {
+                parts[2 * warp + which] = Part{item_begin, item_end, cu0, sw.n, h, rt};
+            }
             u = seg_end;
             ++item;
         }
@@ -896,114 +904,107 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
     if (*abort_flag) return;
 
     // ---- items shared by warps ----
+    // lane i < 2 WARPS stands for parts[i]; `heads`: the first part of each item
+    const int64_t my_end = lane < 2 * WARPS ? parts[lane].item_end : 0;
+    const int64_t my_begin = lane < 2 * WARPS ? parts[lane].item_begin : 0;
+    const uint32_t valid = __ballot_sync(0xFFFFFFFFu, my_end != 0);
+    const uint32_t below = valid & ((1u << lane) - 1u);
+    const int64_t prev_begin = __shfl_sync(0xFFFFFFFFu, my_begin, below ? 31 - __clz(below) : 0);
+    const uint32_t heads = __ballot_sync(0xFFFFFFFFu, my_end != 0 && (!below || prev_begin != my_begin));
+    const uint32_t shared = __ballot_sync(
+        0xFFFFFFFFu, my_end != 0 && (my_begin < cta_begin || my_end > cta_end));
     auto slot_of = [&](int i) {                     // of parts[i]
         return reinterpret_cast<const float *>(
             smem + ((i & 1) ? L::ring_off + (i >> 1) * L::ring : L::first_off + (i >> 1) * L::slot));
     };
-    // per part and row: its factor, and the item's maximum and sum
-    for (int e = tid; e < 2 * WARPS * R; e += kThreads) {
-        const int i = e / R, row = e - i * R;
-        if (parts[i].item_end == 0) continue;
-        float n = kNoMax, l = 0.0f;
-        for (int j = 0; j < 2 * WARPS; ++j)
-            if (parts[j].item_end != 0 && parts[j].item_begin == parts[i].item_begin)
-                n = fmaxf(n, slot_of(j)[SL::stats + row]);
-        for (int j = 0; j < 2 * WARPS; ++j)
-            if (parts[j].item_end != 0 && parts[j].item_begin == parts[i].item_begin)
-                l += slot_of(j)[SL::stats + R + row] * ex2(slot_of(j)[SL::stats + row] - n);
-        part_w[i][row] = ex2(slot_of(i)[SL::stats + row] - n);
-        part_n[i][row] = n;
-        part_l[i][row] = l;
-    }
-    __syncthreads();
-    int pend0 = -1, pend1 = -1;                     // first parts of items shared with other CTAs
-    for (int i = 0; i < 2 * WARPS;) {
-        if (parts[i].item_end == 0) { ++i; continue; }
-        const Part it = parts[i];
-        int j = i + 1;                              // parts i .. j - 1 are the item's
-        while (j < 2 * WARPS && (parts[j].item_end == 0 || parts[j].item_begin == it.item_begin)) ++j;
-        float *part_dst = nullptr;
-        if (it.item_begin < cta_begin || it.item_end > cta_end) {
-            const int sl = partial_slot(it.item_begin, cta_begin);
-            part_dst = p.partials + ((int64_t)blockIdx.x * 2 + sl) * SL::floats;
-            if (sl) pend1 = i;
-            else pend0 = i;
-        }
-        const int cu0 = p.cu[it.b], n = p.cu[it.b + 1] - cu0;
+    for (uint32_t todo = heads; todo; todo &= todo - 1) {
+        const int i = __ffs(todo) - 1;
+        const uint32_t rest = todo & (todo - 1);
+        const uint32_t mine = valid & (rest ? (1u << (__ffs(rest) - 1)) - 1u : ~0u) & ~((1u << i) - 1u);
+        const bool out_of_cta = (shared >> i) & 1u;
+        float *part_dst = p.partials + ((int64_t)blockIdx.x * 2 +
+                                        partial_slot(parts[i].item_begin, cta_begin)) * SL::floats;
         for (int e = tid; e < R * D / 4; e += kThreads) {
-            const int row = e / (D / 4), d = 4 * (e - row * (D / 4));
+            const int row = e / (D / 4), d = 4 * (e % (D / 4));
+            float n = kNoMax, l = 0.0f;
             float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            for (int x = i; x < j; ++x) {
-                if (parts[x].item_end == 0) continue;
-                const float4 v = *reinterpret_cast<const float4 *>(slot_of(x) + row * SL::pitch + d);
-                const float w = part_w[x][row];
+            for (uint32_t x = mine; x; x &= x - 1) n = fmaxf(n, slot_of(__ffs(x) - 1)[SL::stats + row]);
+            for (uint32_t x = mine; x; x &= x - 1) {
+                const float *q = slot_of(__ffs(x) - 1);
+                const float w = ex2(q[SL::stats + row] - n);
+                const float4 v = *reinterpret_cast<const float4 *>(q + row * SL::pitch + d);
+                l += w * q[SL::stats + R + row];
                 o.x += w * v.x; o.y += w * v.y; o.z += w * v.z; o.w += w * v.w;
             }
-            if (part_dst) {
+            if (out_of_cta) {
                 __stcg(reinterpret_cast<float4 *>(part_dst + row * SL::pitch + d), o);
                 if (d == 0) {
-                    __stcg(part_dst + SL::stats + row, part_n[i][row]);
-                    __stcg(part_dst + SL::stats + R + row, part_l[i][row]);
+                    __stcg(part_dst + SL::stats + row, n);
+                    __stcg(part_dst + SL::stats + R + row, l);
                 }
-            } else if (uint16_t *dst = out_row<D>(p, cu0, n, it.h, it.rt * R + row)) {
-                store4(dst + d, o, row_factor(part_l[i][row]));
+            } else {
+                const Part &it = parts[i];
+                if (uint16_t *dst = out_row<D>(p, it.cu0, it.n, it.h, it.rt * R + row))
+                    store4(dst + d, o, row_factor(l));
             }
         }
-        i = j;
     }
-    if (pend0 < 0 && pend1 < 0) return;
+    if (!shared) return;
     // ---- items shared by CTAs: the last to arrive adds the parts in order ----
-    __threadfence();
+    const uint32_t ends = heads & shared;           // one or two items
     __syncthreads();
     if (tid < 2) {
-        const int pi = tid ? pend1 : pend0;
         last_flag[tid] = 0;
-        if (pi >= 0) {
-            const int64_t c0 = parts[pi].item_begin / quota, c1 = (parts[pi].item_end - 1) / quota;
+        const uint32_t x = tid ? ends & (ends - 1) : ends;
+        if (x) {
+            const Part &it = parts[__ffs(x) - 1];
+            const int64_t c0 = it.item_begin / quota, c1 = (it.item_end - 1) / quota;
+            __threadfence();                        // this CTA's parts, ordered by the barrier
             last_flag[tid] = atomicAdd(&p.counters[c0], 1u) == (uint32_t)(c1 - c0);
+            __threadfence();
         }
     }
     __syncthreads();
-    float *factors = reinterpret_cast<float *>(smem);       // [parts][R]; the rings are idle
-    for (int sl = 0; sl < 2; ++sl) {
-        if (!last_flag[sl]) continue;
-        __threadfence();
-        const Part it = parts[sl ? pend1 : pend0];
+    for (int k = 0; k < 2; ++k) {
+        if (!last_flag[k]) continue;
+        const Part it = parts[__ffs(k ? ends & (ends - 1) : ends) - 1];
         const int64_t c0 = it.item_begin / quota;
         const int count = (int)((it.item_end - 1) / quota - c0) + 1;
         const int s0 = partial_slot(it.item_begin, range_begin(c0, quota, units));
         const float *base = p.partials + 2 * c0 * SL::floats;
         auto part = [&](int x) { return base + (int64_t)(2 * x + (x == 0 ? s0 : 0)) * SL::floats; };
-        for (int row = warp; row < R; row += WARPS) {
-            float n = kNoMax, l = 0.0f;
-            for (int x = lane; x < count; x += 32) n = fmaxf(n, __ldcg(part(x) + SL::stats + row));
-#pragma unroll
-            for (int o = 16; o; o >>= 1) n = fmaxf(n, __shfl_xor_sync(0xFFFFFFFFu, n, o));
-            for (int x = lane; x < count; x += 32) {
-                const float w = ex2(__ldcg(part(x) + SL::stats + row) - n);
-                factors[x * R + row] = w;
-                l += __ldcg(part(x) + SL::stats + R + row) * w;
-            }
-#pragma unroll
-            for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
-            if (lane == 0) part_l[0][row] = l;
-        }
-        __syncthreads();
-        const int cu0 = p.cu[it.b], n = p.cu[it.b + 1] - cu0;
         for (int e = tid; e < R * D / 4; e += kThreads) {
-            const int row = e / (D / 4), d = 4 * (e - row * (D / 4));
+            const int row = e / (D / 4), d = 4 * (e % (D / 4));
+            // parts in fours, each four's loads together
+            float n = kNoMax, l = 0.0f;
             float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-            for (int x = 0; x < count; ++x) {
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(part(x) + row * SL::pitch + d));
-                const float w = factors[x * R + row];
-                o.x += w * v.x; o.y += w * v.y; o.z += w * v.z; o.w += w * v.w;
+            for (int x0 = 0; x0 < count; x0 += 4) {
+                float pn[4], pl[4];
+                float4 v[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const float *q = part(min(x0 + y, count - 1));
+                    pn[y] = __ldcg(q + SL::stats + row);
+                    pl[y] = __ldcg(q + SL::stats + R + row);
+                    v[y] = __ldcg(reinterpret_cast<const float4 *>(q + row * SL::pitch + d));
+                }
+                float n2 = n;
+#pragma unroll
+                for (int y = 0; y < 4; ++y) n2 = fmaxf(n2, pn[y]);
+                const float f = ex2(n - n2);
+                l *= f; o.x *= f; o.y *= f; o.z *= f; o.w *= f;
+                n = n2;
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const float w = x0 + y < count ? ex2(pn[y] - n) : 0.0f;
+                    l += w * pl[y];
+                    o.x += w * v[y].x; o.y += w * v[y].y; o.z += w * v[y].z; o.w += w * v[y].w;
+                }
             }
-            if (uint16_t *dst = out_row<D>(p, cu0, n, it.h, it.rt * R + row))
-                store4(dst + d, o, row_factor(part_l[0][row]));
+            if (uint16_t *dst = out_row<D>(p, it.cu0, it.n, it.h, it.rt * R + row))
+                store4(dst + d, o, row_factor(l));
         }
         if (tid == 0) p.counters[c0] = 0u;
-        __syncthreads();
     }
 }
 
