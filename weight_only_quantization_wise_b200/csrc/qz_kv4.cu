@@ -213,16 +213,24 @@ __global__ void __launch_bounds__(32 * kStoreWarps) kv4_read_kernel(const StoreA
 // p = len - n + i and sees keys j <= p (and j > p - window):
 //   s_j = scale sum_d q_d S_j (c_jd - Z_j),  P = softmax(s),
 //   out_d = sum_j P_j S_j (c_jd - Z_j).
-// The codes enter the tensor cores as the exact fp16 integers c - Z.  Of a
-// 16-bit half, nibble 0 ORed under fp16 1024 is 1024 + c and nibble 1 under 64
-// is 64 + c (one LOP3 each for the same nibble of both halves), and one packed
-// subtraction of 1024 + Z or 64 + Z leaves c - Z; a shift by 8 does the other
-// two.  (Leaving the subtraction out -- codes as fp16 subnormals, Z taken off
-// the sums -- saves 4 instructions per word, but the tensor core aligns a
-// subnormal's products by its nominal exponent and loses their low bits:
-// 2^-15 of the largest product, seen where one key holds the weight and c = Z.)
-// Queries are bf16 brought into fp16's range by a power of two per row (exact
-// above 2^-24 of the row's largest value).  S stays out of the first product.
+// Scores are integer products: a row's query is a 16-bit fixed-point number
+// relative to its largest value (q = i 2^-e, |i| < 2^15: at most 2^-15 of that
+// value off; bf16 values down to 2^-7 of it are exact), split into a signed
+// high and an unsigned low byte, and the codes are the bytes of a word ANDed
+// with 0x0F0F0F0F, and shifted by 4: 3 instructions for 8 codes, two mma.sync
+// m16n8k32 with exact 32-bit sums.  Z and S stay out of the product:
+//   sum_d q_d S (c - Z) = S 2^-e (sum_d i_d c - Z sum_d i_d).
+// (As fp16 products with c - Z formed per code, the scores took 9 instructions
+// for 8 codes; the kernel is bound by its instructions.)
+// For the values the codes enter the tensor cores as the exact fp16 integers
+// c - Z.  Of a 16-bit half, nibble 0 ORed under fp16 1024 is 1024 + c and
+// nibble 1 under 64 is 64 + c (one LOP3 each for the same nibble of both
+// halves), and one packed subtraction of 1024 + Z or 64 + Z leaves c - Z; a
+// shift by 8 does the other two.  (Leaving the subtraction out -- codes as fp16
+// subnormals, Z taken off the sums -- saves 4 instructions per word, but the
+// tensor core aligns a subnormal's products by its nominal exponent and loses
+// their low bits: 2^-15 of the largest product, seen where one key holds the
+// weight and c = Z.)
 // The weights w_j = P_j S_j are rounded once to fp16 (2^-11 of each) for the
 // second product.  One running maximum n per row, of s_j + log2 S_j (all in
 // powers of two), scales both sums: w_j = 2^(s_j - n) S_j lies below 2^4
@@ -339,6 +347,25 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// Integer product of 4-bit codes (u8) with query bytes, m16n8k32, from zero
+// or added to c.
+template <bool ADD, bool SIGNED>
+__device__ __forceinline__ void mma_i8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                       uint32_t a3, uint32_t b0, uint32_t b1) {
+    const int z0 = ADD ? c[0] : 0, z1 = ADD ? c[1] : 0, z2 = ADD ? c[2] : 0, z3 = ADD ? c[3] : 0;
+    if (SIGNED)
+        asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 "
+            "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+            : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(z0), "r"(z1), "r"(z2),
+              "r"(z3));
+    else
+        asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.u8.s32 "
+            "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+            : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(z0), "r"(z1), "r"(z2),
+              "r"(z3));
+}
 __device__ __forceinline__ float bf16_at(const uint8_t *q) {
     return __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(q) << 16);
 }
@@ -351,9 +378,8 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_
 
 // mbar_wait that reads the clock only after 64 polls (each may suspend the
 // warp for up to a microsecond): the waits here are short and frequent.
-__device__ __forceinline__ bool ring_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns,
-                                          volatile uint32_t *abort_flag, unsigned int *err_word) {
-    if (mbar_try_wait(bar, parity)) return true;
+__device__ __noinline__ bool ring_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns,
+                                       volatile uint32_t *abort_flag, unsigned int *err_word) {
     for (int i = 0; i < 64; ++i)
         if (mbar_try_wait_hint(bar, parity, 1000u)) return true;
     return mbar_wait(bar, parity, limit_ns, abort_flag, err_word);
@@ -537,36 +563,46 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
             uint32_t qf[L::q_smem ? 1 : NB][L::q_smem ? 1 : 4 * KW];
             const uint32_t q_area = sbase + L::q_off + (uint32_t)warp * L::q_bytes + 16u * lane;
             float kq[NB][2];                       // per column 2 tig, 2 tig + 1
+            int qsum[NG][NB][2];                   // sum_d i_d of each group
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
                 const uint4 (&x)[KW] = qx[nb];
-                float big = 0.0f;
+                uint32_t big = 0;                  // largest |q|, as bf16 bits (NaN above inf)
 #pragma unroll
                 for (int j = 0; j < KW; ++j) {
                     const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        big = fmaxf(big, fmaxf(fabsf(dev::bf16_lo(w[i])), fabsf(dev::bf16_hi(w[i]))));
+                        big = max(big, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
                 }
-                big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
-                big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
+                big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
+                big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
                 // 2^e brings the largest |q| into [2^14, 2^15) (e <= 126)
-                const int be = (int)(__float_as_uint(big) >> 23);
-                const int e = big > 0.0f ? min(14 + 127 - be, 126) : 0;
+                const int e = big ? min(14 + 127 - (int)(big >> 7), 126) : 0;
                 const float f = __uint_as_float((uint32_t)(e + 127) << 23);
+                int sum[NG];
+#pragma unroll
+                for (int gr = 0; gr < NG; ++gr) sum[gr] = 0;
 #pragma unroll
                 for (int j = 0; j < KW; ++j) {
                     const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-                    float v[8];
+                    int v[8];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        v[2 * i] = dev::bf16_lo(w[i]) * f;
-                        v[2 * i + 1] = dev::bf16_hi(w[i]) * f;
+                        v[2 * i] = __float2int_rn(dev::bf16_lo(w[i]) * f);
+                        v[2 * i + 1] = __float2int_rn(dev::bf16_hi(w[i]) * f);
+                        sum[32 * j / G] += v[2 * i] + v[2 * i + 1];
                     }
-                    // a word's code pairs: nibbles (0,4), (1,5), (2,6), (3,7)
+                    // a word's even nibbles are k 4 tig .. of the product, its odd
+                    // ones k 16 + 4 tig ..: high bytes, then low bytes
                     uint32_t f4[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) f4[i] = pack_f16x2(v[i], v[i + 4]);
+                    for (int odd = 0; odd < 2; ++odd) {
+                        const uint32_t a = dev::prmt(v[odd], v[2 + odd], 0x5140u);
+                        const uint32_t c = dev::prmt(v[4 + odd], v[6 + odd], 0x5140u);
+                        f4[odd] = dev::prmt(a, c, 0x7632u);        // high bytes
+                        f4[2 + odd] = dev::prmt(a, c, 0x5410u);    // low bytes
+                    }
                     if constexpr (L::q_smem) {
                         asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
                                          q_area + 512u * (uint32_t)(j * NB + nb)),
@@ -576,9 +612,19 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                         for (int i = 0; i < 4; ++i) qf[nb][4 * j + i] = f4[i];
                     }
                 }
-                const float kr = p.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23);
+                // a row with an infinity or a NaN gives NaN
+                const float kr = big >= 0x7F80u ? __int_as_float(0x7FFFFFFF)
+                                                : p.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23);
                 kq[nb][0] = __shfl_sync(0xFFFFFFFFu, kr, 8 * tig);
                 kq[nb][1] = __shfl_sync(0xFFFFFFFFu, kr, 8 * tig + 4);
+#pragma unroll
+                for (int gr = 0; gr < NG; ++gr) {
+                    int t = sum[gr];
+                    t += __shfl_xor_sync(0xFFFFFFFFu, t, 1);
+                    t += __shfl_xor_sync(0xFFFFFFFFu, t, 2);
+                    qsum[gr][nb][0] = __shfl_sync(0xFFFFFFFFu, t, 8 * tig);
+                    qsum[gr][nb][1] = __shfl_sync(0xFFFFFFFFu, t, 8 * tig + 4);
+                }
             }
             // keys each column's row may see: [klo, khi)
             int khi[NB][2], klo[NB][2];
@@ -609,12 +655,13 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                 }
             }
             for (int i = 0; i < steps; ++i) {
-                ok = ring_wait(bar0 + 8u * stage, phase, p.wait_limit, abort_flag, p.err_word);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                
-                if (!ok) {
-                    in_flight = min(S, steps - i);
-                    break;
+                if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(bar0 + 8u * stage, phase))) {
+                    ok = ring_wait(bar0 + 8u * stage, phase, p.wait_limit, abort_flag, p.err_word);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) {
+                        in_flight = min(S, steps - i);
+                        break;
+                    }
                 }
                 const int key0 = (blk0 + 2 * i) * kBlock;
                 const uint32_t got = (have >> (2 * stage)) & 3u;
@@ -641,64 +688,54 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                         }
 #pragma unroll
                     for (int gr = 0; gr < NG; ++gr) {
-                        float t[2][NB][4];
-                        uint32_t z1[2][2], z2[2][2];
-#pragma unroll
-                        for (int rc = 0; rc < 2; ++rc) {
-#pragma unroll
-                            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                                for (int c = 0; c < 4; ++c) t[rc][nb][c] = 0.0f;
-#pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                const uint32_t z = sr[rc][k_zeros_off(D, NG) + 16 * gr + gid + 8 * x];
-                                z1[rc][x] = z * 0x00010001u + 0x64006400u;
-                                z2[rc][x] = z * 0x00100010u + 0x54005400u;
-                            }
-                        }
+                        int th[2][NB][4], tl[2][NB][4];    // high and low bytes of the queries
 #pragma unroll
                         for (int jj = 0; jj < G / 32; ++jj) {
                             const int j = gr * (G / 32) + jj;
-                            uint4 qv[L::q_smem ? NB : 1];
-                            if constexpr (L::q_smem)
+                            uint4 qv[NB];
 #pragma unroll
-                                for (int nb = 0; nb < NB; ++nb)
+                            for (int nb = 0; nb < NB; ++nb) {
+                                if constexpr (L::q_smem)
                                     qv[nb] = *reinterpret_cast<const uint4 *>(
                                         smem + L::q_off + warp * L::q_bytes + 16 * lane +
                                         512 * (j * NB + nb));
+                                else
+                                    qv[nb] = make_uint4(qf[nb][4 * j], qf[nb][4 * j + 1],
+                                                        qf[nb][4 * j + 2], qf[nb][4 * j + 3]);
+                            }
 #pragma unroll
-                            for (int half = 0; half < 2; ++half)
+                            for (int rc = 0; rc < 2; ++rc) {
+                                const uint32_t a = kw[rc][0][j], c = kw[rc][1][j];
+                                const uint32_t a0 = a & 0x0F0F0F0Fu, a1 = c & 0x0F0F0F0Fu;
+                                const uint32_t a2 = (a >> 4) & 0x0F0F0F0Fu, a3 = (c >> 4) & 0x0F0F0F0Fu;
 #pragma unroll
-                                for (int rc = 0; rc < 2; ++rc) {
-                                    const uint32_t a = kw[rc][0][j] >> (8 * half);
-                                    const uint32_t c = kw[rc][1][j] >> (8 * half);
-                                    const uint32_t a0 = codes_lo(a, z1[rc][0]), a1 = codes_lo(c, z1[rc][1]);
-                                    const uint32_t a2 = codes_hi(a, z2[rc][0]), a3 = codes_hi(c, z2[rc][1]);
-#pragma unroll
-                                    for (int nb = 0; nb < NB; ++nb) {
-                                        if constexpr (L::q_smem)
-                                            mma_f16(t[rc][nb], a0, a1, a2, a3,
-                                                    half ? qv[nb].z : qv[nb].x,
-                                                    half ? qv[nb].w : qv[nb].y);
-                                        else
-                                            mma_f16(t[rc][nb], a0, a1, a2, a3,
-                                                    qf[nb][4 * j + 2 * half],
-                                                    qf[nb][4 * j + 2 * half + 1]);
+                                for (int nb = 0; nb < NB; ++nb) {
+                                    if (jj == 0) {
+                                        mma_i8<false, true>(th[rc][nb], a0, a1, a2, a3, qv[nb].x, qv[nb].y);
+                                        mma_i8<false, false>(tl[rc][nb], a0, a1, a2, a3, qv[nb].z, qv[nb].w);
+                                    } else {
+                                        mma_i8<true, true>(th[rc][nb], a0, a1, a2, a3, qv[nb].x, qv[nb].y);
+                                        mma_i8<true, false>(tl[rc][nb], a0, a1, a2, a3, qv[nb].z, qv[nb].w);
                                     }
                                 }
+                            }
                         }
 #pragma unroll
                         for (int rc = 0; rc < 2; ++rc)
 #pragma unroll
                             for (int x = 0; x < 2; ++x) {
+                                const int z = sr[rc][k_zeros_off(D, NG) + 16 * gr + gid + 8 * x];
                                 const float sc = bf16_at(sr[rc] + k_scales_off(D) + 32 * gr + 2 * (gid + 8 * x));
 #pragma unroll
                                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                                    for (int c = 0; c < 2; ++c)
+                                    for (int c = 0; c < 2; ++c) {
+                                        const float t = (float)(th[rc][nb][2 * x + c] * 256 +
+                                                                tl[rc][nb][2 * x + c] -
+                                                                z * qsum[gr][nb][c]);
                                         s[rc][nb][2 * x + c] =
-                                            gr == 0 ? t[rc][nb][2 * x + c] * sc
-                                                    : fmaf(t[rc][nb][2 * x + c], sc, s[rc][nb][2 * x + c]);
+                                            gr == 0 ? t * sc : fmaf(t, sc, s[rc][nb][2 * x + c]);
+                                    }
                             }
                     }
                     // -- V scales, log2 of the largest
@@ -746,16 +783,19 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                                             s[rc][nb][2 * x + c] = __int_as_float(0xFF800000);
                             }
                     }
-                    // -- running maximum: raised only when a weight would be 2^4 or
-                    //    more (fp16 holds weights below 2^16)
+                    // -- s minus the running maximum; the maximum is raised only when
+                    //    a weight would be 2^4 or more (fp16 holds those below 2^16)
+                    float y[2][NB][4];
                     bool raise = false;
 #pragma unroll
                     for (int rc = 0; rc < 2; ++rc)
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                            for (int c = 0; c < 4; ++c)
-                                raise |= s[rc][nb][c] + vl[rc][c >> 1] > nm[nb][c & 1] + 4.0f;
+                            for (int c = 0; c < 4; ++c) {
+                                y[rc][nb][c] = s[rc][nb][c] - nm[nb][c & 1];
+                                raise |= y[rc][nb][c] > 4.0f - vl[rc][c >> 1];
+                            }
                     if (__any_sync(0xFFFFFFFFu, raise)) {
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb)
@@ -771,9 +811,14 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                                 nm[nb][c] = d;
                                 l[nb][c] *= fo;
 #pragma unroll
-                                for (int y = 0; y < 4 * VW; ++y) {
-                                    acc[y][nb][c] *= fo;
-                                    acc[y][nb][c + 2] *= fo;
+                                for (int rc = 0; rc < 2; ++rc) {
+                                    y[rc][nb][c] = s[rc][nb][c] - d;
+                                    y[rc][nb][c + 2] = s[rc][nb][c + 2] - d;
+                                }
+#pragma unroll
+                                for (int z = 0; z < 4 * VW; ++z) {
+                                    acc[z][nb][c] *= fo;
+                                    acc[z][nb][c + 2] *= fo;
                                 }
                             }
                     }
@@ -786,8 +831,8 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                             for (int x = 0; x < 2; ++x) {
-                                const float p0 = ex2(s[rc][nb][2 * x] - nm[nb][0]);
-                                const float p1 = ex2(s[rc][nb][2 * x + 1] - nm[nb][1]);
+                                const float p0 = ex2(y[rc][nb][2 * x]);
+                                const float p1 = ex2(y[rc][nb][2 * x + 1]);
                                 l[nb][0] += p0;
                                 l[nb][1] += p1;
 #pragma unroll
