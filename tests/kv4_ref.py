@@ -75,7 +75,7 @@ def attention(q, kv, lens, new, scale, window, masked=None):
 
     q: (T, Hq, D) float64; kv: list of (k^, v^, S_v max per key) per sequence,
     each (len, H, D) float64.  masked[b]: keys to leave out.  Returns out, and
-    per output the bound's parts: sum P|v|, sum P S, max P S, the score error.
+    per output the bound's parts: sum P|v|, sum P S, max P S, |scale| max|q| sum|k|.
     """
     T, Hq, D = q.shape
     out = np.zeros((T, Hq, D))
@@ -105,7 +105,7 @@ def attention(q, kv, lens, new, scale, window, masked=None):
                     parts["pv"][row, h] = P @ np.abs(vh)
                     parts["ps"][row, h] = (P * S).sum()
                     parts["mps"][row, h] = (P * S).max()
-                    parts["dq"][row, h] = abs(scale) * 15 * np.abs(qh).sum() * sk[:, h // G].max()
+                    parts["dq"][row, h] = abs(scale) * np.abs(qh).max() * np.abs(kh).sum(-1).max()
                     parts["keys"][row, h] = keep.sum()
             row += 1
     return out, parts
@@ -116,15 +116,17 @@ def bound(out, parts, D):
 
     bf16 result: half a step, 2^-8 of the value.  Weights P S rounded to fp16:
     2^-11 of each, or 2^-25 absolute below its normal range, in units of which
-    the largest weight is at least 2^-1 (S lies in the upper half of its
-    binade's bound): per key 15 * 2^-24 of the largest P S.  Scores: the tensor
-    core adds 16 products and the accumulator with an error of at most 2^-22
-    of the largest magnitude each time, D / 16 times, and a few fp32 roundings
-    more: delta = |scale| 15 S sum|q| 2^-22 (D / 16 + 4), which moves each P by
-    a factor of at most e^(2 delta); ex2 and the fp32 sums add 2^-20.  The sum
-    over keys: 2^-22 of sum P S 15 per step of 16 keys.
+    the largest weight is at least 2^-1 (log2 S is within 2^-20): per key
+    15 * 2^-24 of the largest P S.  Scores: a query is held in 16 bits relative
+    to its largest value, at most 2^-15 of that off, so a score moves by at most
+    |scale| 2^-15 max|q| sum|k|; its integer sum is exact, and the conversion
+    and two products round it by less than 2^-21 of |scale| max|q| sum|k|.
+    That moves each P by a factor of at most e^(2 delta); ex2 and the fp32 sums
+    add 2^-20.  The sum over keys: the tensor core adds 16 products and the
+    accumulator with an error of at most 2^-22 of the largest magnitude, sum P S
+    15, each time.
     """
-    delta = parts["dq"] * 2.0 ** -22 * (D / 16 + 4)
+    delta = parts["dq"] * (2.0 ** -15 + 2.0 ** -21)
     return (2.0 ** -8 * np.abs(out) +
             (2.0 ** -11 + 2.0 ** -20 + np.expm1(2 * delta)) * parts["pv"] * (1 + 2.0 ** -8) +
             (parts["keys"] / 16 + 8) * 2.0 ** -22 * 15 * parts["ps"] +

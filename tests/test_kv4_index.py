@@ -28,7 +28,7 @@ int s_off(int D, int ng, int which) {
                       k_zeros_off(D, ng), v_zeros_off(D, ng)};
     return o[which];
 }
-ll s_record_index(const int *row, ll max_pages, ll num_pages, ll heads, ll h, int pb, ll block) {
+ll s_record_index(const int *row, ll max_pages, ll num_pages, int heads, int h, int pb, int block) {
     return record_index(row, max_pages, num_pages, heads, h, pb, block);
 }
 ll s_find_sequence(const int *cu, ll B, ll t) { return find_sequence(cu, B, t); }
@@ -38,7 +38,10 @@ void s_seq_work(int cu0, int cu1, int len, int T, int cap, int win, int share, i
     o[0] = s.n; o[1] = s.len; o[2] = s.block0; o[3] = s.blocks; o[4] = s.row_tiles; o[5] = s.units;
 }
 ll s_range_begin(ll c, ll q, ll u) { return range_begin(c, q, u); }
-ll s_cta_quota(ll u, ll c, ll m) { return cta_quota(u, c, m); }
+ll s_cta_quota(ll u, ll items, int blocks, ll c, int m, int w) {
+    return cta_quota(u, items, blocks, c, m, w);
+}
+ll s_quotient(ll a, ll b) { return quotient(a, b); }
 int s_warp_quota(ll n, int w) { return warp_quota(n, w); }
 int s_partial_slot(ll a, ll b) { return partial_slot(a, b); }
 }
@@ -55,9 +58,10 @@ def ix(tmp_path_factory):
                     "-o", str(lib)], check=True)
     so = ctypes.CDLL(str(lib))
     ll = ctypes.c_longlong
-    for name, args in (("s_record_index", [ctypes.c_void_p, ll, ll, ll, ll, ctypes.c_int, ll]),
+    for name, args in (("s_record_index", [ctypes.c_void_p, ll, ll] + [ctypes.c_int] * 4),
                        ("s_find_sequence", [ctypes.c_void_p, ll, ll]),
-                       ("s_range_begin", [ll, ll, ll]), ("s_cta_quota", [ll, ll, ll])):
+                       ("s_range_begin", [ll, ll, ll]), ("s_quotient", [ll, ll]),
+                       ("s_cta_quota", [ll, ll, ctypes.c_int, ll, ctypes.c_int, ctypes.c_int])):
         f = getattr(so, name)
         f.argtypes, f.restype = args, ll
     so.s_seq_work.argtypes = [ctypes.c_int] * 9 + [ctypes.c_void_p]
@@ -133,6 +137,11 @@ def test_record_offsets_past_32_bits(ix):
     assert got == ((2 ** 31 - 2) * 8 + 7) * 4 + 3
 
 
+def test_quotient(ix):
+    for a, b in [(0, 1), (7, 7), (2 ** 32 - 1, 3), (2 ** 32, 3), (2 ** 40 + 5, 2 ** 33), (9, 2 ** 35)]:
+        assert ix.s_quotient(a, b) == a // b
+
+
 def test_find_sequence(ix):
     rng = random.Random(6)
     for _ in range(100):
@@ -179,8 +188,10 @@ def test_work_split(ix, case):
     if units == 0:
         return
     begins = np.cumsum([0] + items)
-    quota = ix.s_cta_quota(units, grid, min_units)
+    quota = ix.s_cta_quota(units, len(items), max(items), grid, min_units, 96)
     assert quota >= min_units and quota * grid >= units
+    if len(set(items)) == 1 and items[0] <= 96:
+        assert quota >= items[0]
     covered, homes, slots, active = 0, {}, {}, 0
     for c in range(grid):
         b0, b1 = ix.s_range_begin(c, quota, units), ix.s_range_begin(c + 1, quota, units)

@@ -477,42 +477,71 @@ def qz_kv4_cache_bytes(num_pages, kv_heads, head_dim, page_size, group_size=128)
     return v
 
 
-def _device_guard(dev):
-    """Makes `dev` current for a launch when it is not."""
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
+_NO_SCOPE = contextlib.nullcontext()
+
+
+class _Scope:
+    """Makes `dev` (and `stream`) current for a call's allocations and launch."""
+
+    def __init__(self, dev, stream):
+        self.dev, self.stream = dev, stream
+
+    def __enter__(self):
+        self.guard = torch.cuda.device(self.dev)
+        self.guard.__enter__()
+        self.on = _on(self.stream)
+        self.on.__enter__()
+
+    def __exit__(self, *exc):
+        self.on.__exit__(*exc)
+        self.guard.__exit__(*exc)
+
+
+def _scope(dev, stream):
+    if stream is None and dev.index == torch.cuda.current_device():
+        return _NO_SCOPE
+    return _Scope(dev, stream)
+
+
+def _stream_of(dev, stream):
+    """Handle of the stream a call runs on: `stream`, else `dev`'s current one."""
+    return (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
 
 
 def _heads(t, name, dev):
-    """Pointer and token stride of a (T, heads, head_dim) bf16 tensor whose
+    """Address and token stride of a (T, heads, head_dim) bf16 tensor whose
     heads and values are contiguous (tokens may lie further apart)."""
-    if t.dtype != torch.bfloat16 or t.dim() != 3:
-        raise ValueError(f"{name} must be a (tokens, heads, head_dim) bf16 tensor")
-    if t.device != dev or not t.is_cuda:
-        raise ValueError(f"{name} must live on the cache's CUDA device")
+    if t.dtype is not torch.bfloat16 or t.dim() != 3 or t.device != dev:
+        raise ValueError(f"{name} must be a (tokens, heads, head_dim) bf16 tensor on the "
+                         "cache's device")
     n, h, d = t.shape
+    if t.is_contiguous():
+        return t.data_ptr(), h * d
     st = t.stride()
     if (d > 1 and st[2] != 1) or (h > 1 and st[1] != d):
         raise ValueError(f"{name}: heads and values of a token must be contiguous")
-    return ctypes.c_void_p(t.data_ptr()), (st[0] if n > 1 else h * d)
+    return t.data_ptr(), (st[0] if n > 1 else h * d)
 
 
 def _kv4_args(cache, page_table, kv_lens, cu_tokens, kv_heads, head_dim, page_size, group_size):
-    """Pointers of the four shared arrays, B, pages in the cache, pages per sequence."""
+    """Addresses of the four shared arrays, B, pages in the cache, pages per sequence."""
     dev = cache.device
-    for t, name, dim in ((page_table, "page_table", 2), (kv_lens, "kv_lens", 1),
-                         (cu_tokens, "cu_tokens", 1)):
-        if t.dtype != torch.int32 or t.dim() != dim or t.device != dev:
-            raise ValueError(f"{name} must be a {dim}-D int32 tensor on the cache's device")
-    B = kv_lens.shape[0]
-    if page_table.shape[0] != B or cu_tokens.shape[0] != B + 1:
+    i32 = torch.int32
+    if not (cache.is_cuda and cache.dtype is torch.uint8 and cache.is_contiguous()):
+        raise ValueError("cache must be a contiguous uint8 tensor on a CUDA device")
+    if not (page_table.dtype is i32 and kv_lens.dtype is i32 and cu_tokens.dtype is i32 and
+            page_table.device == dev and kv_lens.device == dev and cu_tokens.device == dev and
+            page_table.is_contiguous() and kv_lens.is_contiguous() and cu_tokens.is_contiguous()):
+        raise ValueError("page_table, kv_lens and cu_tokens must be contiguous int32 tensors on "
+                         "the cache's device")
+    if page_table.dim() != 2 or kv_lens.dim() != 1 or cu_tokens.dim() != 1:
+        raise ValueError("page_table must be 2-D, kv_lens and cu_tokens 1-D")
+    B, width = page_table.shape
+    if kv_lens.shape[0] != B or cu_tokens.shape[0] != B + 1:
         raise ValueError("page_table, kv_lens and cu_tokens must have B, B and B + 1 rows")
-    if cache.dtype != torch.uint8:
-        raise ValueError("cache must be a uint8 tensor")
     pages = cache.numel() // qz_kv4_cache_bytes(1, kv_heads, head_dim, page_size, group_size)
-    return (_ptr(cache), _ptr(page_table), _ptr(kv_lens), _ptr(cu_tokens), B, pages,
-            page_table.shape[1])
+    return (cache.data_ptr(), page_table.data_ptr(), kv_lens.data_ptr(), cu_tokens.data_ptr(), B,
+            pages, width)
 
 
 def qz_kv4_append(cache, k, v, page_table, kv_lens, cu_tokens, page_size, group_size=128,
@@ -535,10 +564,11 @@ def qz_kv4_append(cache, k, v, page_table, kv_lens, cu_tokens, page_size, group_
                                                page_size, group_size)
     if T == 0:
         return
-    st = _launch_stream(stream, dev)
-    with _device_guard(dev):
-        _check(lib.qz_kv4_append(c, kp, vp, ks, vs, pt, kl, cu, T, B, H, D, page_size, group_size,
-                                 pages, width, _handle(st)), "qz_kv4_append")
+    with _scope(dev, stream):
+        status = lib.qz_kv4_append(c, kp, vp, ks, vs, pt, kl, cu, T, B, H, D, page_size,
+                                   group_size, pages, width, _stream_of(dev, stream))
+    if status:
+        raise QzError(status, "qz_kv4_append")
 
 
 def qz_kv4_read(cache, page_table, kv_lens, cu_tokens, tokens, kv_heads, head_dim, page_size,
@@ -550,19 +580,22 @@ def qz_kv4_read(cache, page_table, kv_lens, cu_tokens, tokens, kv_heads, head_di
                                                head_dim, page_size, group_size)
     shape = (tokens, kv_heads, head_dim)
     for t in (k, v):
-        if t is not None and (t.dtype != torch.bfloat16 or tuple(t.shape) != shape or
-                              t.device != dev):
-            raise ValueError("k and v must be (tokens, kv_heads, head_dim) bf16 tensors")
-    st = _launch_stream(stream, dev)
-    with _on(stream), _device_guard(dev):
+        if t is not None and (t.dtype is not torch.bfloat16 or tuple(t.shape) != shape or
+                              t.device != dev or not t.is_contiguous()):
+            raise ValueError("k and v must be contiguous (tokens, kv_heads, head_dim) bf16 tensors "
+                             "on the cache's device")
+    with _scope(dev, stream):
         if k is None:
             k = torch.empty(shape, dtype=torch.bfloat16, device=dev)
         if v is None:
             v = torch.empty(shape, dtype=torch.bfloat16, device=dev)
         if tokens == 0:
             return k, v
-        _check(lib.qz_kv4_read(c, pt, kl, cu, tokens, B, kv_heads, head_dim, page_size, group_size,
-                               pages, width, _ptr(k), _ptr(v), _handle(st)), "qz_kv4_read")
+        status = lib.qz_kv4_read(c, pt, kl, cu, tokens, B, kv_heads, head_dim, page_size,
+                                 group_size, pages, width, k.data_ptr(), v.data_ptr(),
+                                 _stream_of(dev, stream))
+    if status:
+        raise QzError(status, "qz_kv4_read")
     return k, v
 
 
@@ -576,8 +609,7 @@ def qz_kv4_attention(q, cache, page_table, kv_lens, cu_tokens, kv_heads, page_si
     T, H, D = q.shape
     c, pt, kl, cu, B, pages, width = _kv4_args(cache, page_table, kv_lens, cu_tokens, kv_heads, D,
                                                page_size, group_size)
-    st = _launch_stream(stream, dev)
-    with _on(stream), _device_guard(dev):
+    with _scope(dev, stream):
         if out is None:
             out = torch.empty((T, H, D), dtype=torch.bfloat16, device=dev)
         elif out.shape != q.shape:
@@ -587,10 +619,12 @@ def qz_kv4_attention(q, cache, page_table, kv_lens, cu_tokens, kv_heads, page_si
         op, os_ = _heads(out, "out", dev)
         nbytes = qz_workspace_bytes(QZ_OP_KV4_ATTENTION, 1, 1, D, 0)
         ws_ptr, ws_bytes = _ws_args(workspace, nbytes, dev, ("kv4_attention", D))
-        _check(lib.qz_kv4_attention(qp, qs, c, pt, kl, cu, T, B, H, kv_heads, D, page_size,
-                                    group_size, pages, width,
-                                    D ** -0.5 if scale is None else scale, window, op, os_,
-                                    ws_ptr, ws_bytes, _handle(st)), "qz_kv4_attention")
+        status = lib.qz_kv4_attention(qp, qs, c, pt, kl, cu, T, B, H, kv_heads, D, page_size,
+                                      group_size, pages, width,
+                                      D ** -0.5 if scale is None else scale, window, op, os_,
+                                      ws_ptr, ws_bytes, _stream_of(dev, stream))
+    if status:
+        raise QzError(status, "qz_kv4_attention")
     return out
 
 

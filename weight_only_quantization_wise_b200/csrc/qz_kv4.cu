@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(32 * kStoreWarps) kv4_append_kernel(const Stor
     int64_t rec = -1;
     if (pos >= 0)
         rec = record_index(p.page_table + b * p.max_pages, p.max_pages, p.num_pages, p.kv_heads,
-                           h, p.page_size / kBlock, pos / kBlock);
+                           h, p.page_size / kBlock, (int)(pos / kBlock));
     if (rec < 0) {
         if (lane == 0) atomicOr(p.err_word, kErrIndex);
         return;
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(32 * kStoreWarps) kv4_read_kernel(const StoreA
     int64_t rec = -1;
     if (pos >= 0)
         rec = record_index(p.page_table + b * p.max_pages, p.max_pages, p.num_pages, p.kv_heads,
-                           h, p.page_size / kBlock, pos / kBlock);
+                           h, p.page_size / kBlock, (int)(pos / kBlock));
     if (rec < 0) {
         *reinterpret_cast<uint4 *>(ko) = make_uint4(0u, 0u, 0u, 0u);
         *reinterpret_cast<uint4 *>(vo) = make_uint4(0u, 0u, 0u, 0u);
@@ -257,7 +257,7 @@ struct AttnArgs {
     int64_t out_stride;
     float *partials;                   // [ctas][2][Slot]
     uint32_t *counters;                // [ctas]
-    int min_units;
+    int min_units, whole_units;        // see cta_quota
     uint64_t wait_limit;
     unsigned int *err_word;
 };
@@ -418,7 +418,8 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
     constexpr int VW = D / 64;                     // 64-wide spans of d
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t pre[kThreads + 1];          // units before each thread's sequences
-    __shared__ int64_t warp_sum[WARPS];
+    __shared__ int64_t warp_sum[WARPS], warp_items[WARPS];
+    __shared__ int warp_blocks[WARPS];
     __shared__ Part parts[2 * WARPS];
     __shared__ uint32_t abort_word;
     __shared__ int last_flag[2];
@@ -433,11 +434,15 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
 
     // ---- units of all sequences: every CTA adds them up itself ----
     const int per = (p.B + kThreads - 1) / kThreads;           // sequences per thread
-    int64_t scan = 0;
+    int64_t scan = 0, items = 0;
+    int blocks = 0;                                            // of the longest item
     for (int i = 0; i < per; ++i) {
         const int b = tid * per + i;
         if (b < p.B) {
-            scan += work_of(b).units;
+            const SeqWork w = work_of(b);
+            scan += w.units;
+            items += w.row_tiles;
+            if (w.n > 0) blocks = max(blocks, w.blocks);
             const int len = p.kv_lens[b];
             if (blockIdx.x == 0 && (len < 0 || len > p.capacity)) atomicOr(p.err_word, kErrIndex);
         }
@@ -447,7 +452,14 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
         const int64_t v = __shfl_up_sync(0xFFFFFFFFu, scan, o);
         if (lane >= o) scan += v;
     }
-    if (lane == 31) warp_sum[warp] = scan;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) items += __shfl_xor_sync(0xFFFFFFFFu, items, o);
+    blocks = __reduce_max_sync(0xFFFFFFFFu, blocks);
+    if (lane == 31) {
+        warp_sum[warp] = scan;
+        warp_items[warp] = items;
+        warp_blocks[warp] = blocks;
+    }
     if (tid < 2 * WARPS) parts[tid].item_end = 0;
     if (tid == 0) abort_word = 0u;
     if (lane < S) mbar_init(sbase + L::bars_off + 8u * (warp * S + lane), 1);
@@ -458,11 +470,16 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
     for (int w = 0; w < WARPS; ++w) {
         if (w < warp) before += warp_sum[w];
         units += warp_sum[w];
+        if (w != warp) {
+            items += warp_items[w];
+            blocks = max(blocks, warp_blocks[w]);
+        }
     }
     pre[tid + 1] = before + scan;
     if (tid == 0) pre[0] = 0;
     __syncthreads();
-    const int64_t quota = cta_quota(units, gridDim.x, p.min_units);
+    const int64_t quota =
+        cta_quota(units, items * p.kv_heads, blocks, gridDim.x, p.min_units, p.whole_units);
     const int64_t cta_begin = range_begin(blockIdx.x, quota, units);
     const int64_t cta_end = range_begin(blockIdx.x + 1, quota, units);
     if (cta_begin >= cta_end) return;
@@ -493,7 +510,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
             seq_begin += sw.units;
         }
         int64_t u = w_begin;
-        int item = (int)((u - seq_begin) / sw.blocks);         // (head, row tile) of the sequence
+        int item = (int)quotient(u - seq_begin, sw.blocks);         // (head, row tile) of the sequence
         while (u < w_end) {
             while (u >= seq_begin + sw.units) {                // next sequence with units
                 seq_begin += sw.units;
@@ -1003,7 +1020,8 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
         const uint32_t x = tid ? ends & (ends - 1) : ends;
         if (x) {
             const Part &it = parts[__ffs(x) - 1];
-            const int64_t c0 = it.item_begin / quota, c1 = (it.item_end - 1) / quota;
+            const int64_t c0 = quotient(it.item_begin, quota);
+            const int64_t c1 = quotient(it.item_end - 1, quota);
             __threadfence();                        // this CTA's parts, ordered by the barrier
             last_flag[tid] = atomicAdd(&p.counters[c0], 1u) == (uint32_t)(c1 - c0);
             __threadfence();
@@ -1013,8 +1031,8 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
     for (int k = 0; k < 2; ++k) {
         if (!last_flag[k]) continue;
         const Part it = parts[__ffs(k ? ends & (ends - 1) : ends) - 1];
-        const int64_t c0 = it.item_begin / quota;
-        const int count = (int)((it.item_end - 1) / quota - c0) + 1;
+        const int64_t c0 = quotient(it.item_begin, quota);
+        const int count = (int)(quotient(it.item_end - 1, quota) - c0) + 1;
         const int s0 = partial_slot(it.item_begin, range_begin(c0, quota, units));
         const float *base = p.partials + 2 * c0 * SL::floats;
         auto part = [&](int x) { return base + (int64_t)(2 * x + (x == 0 ? s0 : 0)) * SL::floats; };
@@ -1194,7 +1212,10 @@ qz_status launch_kv4_attention(const Kv4Cache &c, const void *q, int64_t q_strid
     // counters first: their place does not depend on the tile size
     p.counters = static_cast<uint32_t *>(workspace);
     p.partials = reinterpret_cast<float *>(static_cast<char *>(workspace) + kCounterBytes);
+    // With fewer than 32 blocks a CTA's prologue and join outweigh its loop (16
+    // and 32 measured alike, 64 slower); whole items up to 96 blocks.
     p.min_units = 32;
+    p.whole_units = 96;
     p.wait_limit = device_wait_limit();
     p.err_word = device_error_word();
     if (p.err_word == nullptr) return QZ_ERR_CUDA;

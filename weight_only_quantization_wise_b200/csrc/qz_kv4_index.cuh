@@ -61,14 +61,21 @@ QZ_HD constexpr int v_unit_byte(int D, int token, int w, int hi, int gid) {
            2 * (token & 1);
 }
 
+// a / b for a >= 0, b > 0; one 32-bit division where both allow it.
+QZ_HD int64_t quotient(int64_t a, int64_t b) {
+    if (((uint64_t)a | (uint64_t)b) >> 32 == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+    return a / b;
+}
+
 // ---- pages --------------------------------------------------------------
 // Record index (in records from the cache's start) of the block of 16 tokens
 // that holds position `pos` of head `h`, or -1 when the page table has no
 // valid page there.  `row` is the sequence's row of the page table.
 QZ_HD int64_t record_index(const int32_t *row, int64_t max_pages, int64_t num_pages,
-                           int64_t kv_heads, int64_t h, int page_blocks, int64_t block) {
-    const int64_t pi = block / page_blocks;
-    if (block < 0 || pi >= max_pages) return -1;
+                           int kv_heads, int h, int page_blocks, int block) {
+    if (block < 0) return -1;
+    const int pi = (int)((uint32_t)block / (uint32_t)page_blocks);
+    if (pi >= max_pages) return -1;
     const int32_t page = row[pi];
     if (page < 0 || page >= num_pages) return -1;
     return ((int64_t)page * kv_heads + h) * page_blocks + (block - pi * page_blocks);
@@ -119,10 +126,16 @@ QZ_HD SeqWork seq_work(int cu0, int cu1, int kv_len, int rows, int capacity, int
 
 // The units of all items, in (sequence, head, row tile, block) order, are cut
 // into contiguous ranges of `quota` units, one per CTA (the last may be
-// shorter): as many CTAs as there are, but none with fewer than min_units.
-QZ_HD int64_t cta_quota(int64_t units, int64_t ctas, int64_t min_units) {
-    const int64_t q = (units + ctas - 1) / ctas;
-    return q > min_units ? q : min_units;
+// shorter): as many CTAs as there are, but none with fewer than min_units.  When
+// all items are alike (`blocks` units each) and short, a CTA takes whole items
+// instead: one more step for its warps costs less than a join through the
+// workspace.
+QZ_HD int64_t cta_quota(int64_t units, int64_t items, int blocks, int64_t ctas, int min_units,
+                        int whole_units) {
+    int64_t q = quotient(units + ctas - 1, ctas);
+    if (q < min_units) q = min_units;
+    if (q < blocks && blocks <= whole_units && items * blocks == units) q = blocks;
+    return q;
 }
 QZ_HD int64_t range_begin(int64_t c, int64_t quota, int64_t units) {
     return c * quota < units ? c * quota : units;
