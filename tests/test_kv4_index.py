@@ -31,7 +31,14 @@ int s_off(int D, int ng, int which) {
 ll s_record_index(const int *row, ll max_pages, ll num_pages, int heads, int h, int pb, int block) {
     return record_index(row, max_pages, num_pages, heads, h, pb, block);
 }
-ll s_find_sequence(const int *cu, ll B, ll t) { return find_sequence(cu, B, t); }
+void s_store_work(int cu0, int cu1, int len, int T, int heads, ll *o) {
+    const StoreWork s = store_work(cu0, cu1, len, T, heads);
+    o[0] = s.n; o[1] = s.block0; o[2] = s.blocks; o[3] = s.first; o[4] = s.units;
+}
+void s_block_range(int cu0, int cu1, int len, int T, int block, int *o) {
+    const StoreWork s = store_work(cu0, cu1, len, T, 1);
+    o[0] = block_lo(s, block); o[1] = block_hi(s, block);
+}
 void s_seq_work(int cu0, int cu1, int len, int T, int cap, int win, int share, int heads, int rows,
                 ll *o) {
     const SeqWork s = seq_work(cu0, cu1, len, T, cap, win, share, heads, rows);
@@ -59,7 +66,6 @@ def ix(tmp_path_factory):
     so = ctypes.CDLL(str(lib))
     ll = ctypes.c_longlong
     for name, args in (("s_record_index", [ctypes.c_void_p, ll, ll] + [ctypes.c_int] * 4),
-                       ("s_find_sequence", [ctypes.c_void_p, ll, ll]),
                        ("s_range_begin", [ll, ll, ll]), ("s_quotient", [ll, ll]),
                        ("s_cta_quota", [ll, ll, ctypes.c_int, ll, ctypes.c_int, ctypes.c_int])):
         f = getattr(so, name)
@@ -67,6 +73,8 @@ def ix(tmp_path_factory):
     so.s_seq_work.argtypes = [ctypes.c_int] * 9 + [ctypes.c_void_p]
     so.s_warp_quota.argtypes = [ll, ctypes.c_int]
     so.s_partial_slot.argtypes = [ll, ll]
+    so.s_store_work.argtypes = [ctypes.c_int] * 5 + [ctypes.c_void_p]
+    so.s_block_range.argtypes = [ctypes.c_int] * 5 + [ctypes.c_void_p]
     return so
 
 
@@ -142,15 +150,21 @@ def test_quotient(ix):
         assert ix.s_quotient(a, b) == a // b
 
 
-def test_find_sequence(ix):
-    rng = random.Random(6)
-    for _ in range(100):
-        counts = [rng.choice([0, 0, 1, 2, 7]) for _ in range(rng.randint(1, 12))]
-        start = rng.choice([0, 0, 3])
-        cu = np.cumsum([start] + counts).astype(np.int32)
-        owner = [-1] * start + [b for b, n in enumerate(counts) for _ in range(n)] + [-1] * 3
-        for t, b in enumerate(owner):
-            assert ix.s_find_sequence(cu.ctypes.data, len(counts), t) == b
+@pytest.mark.parametrize("n", [0, 1, 2, 15, 16, 17, 40])
+@pytest.mark.parametrize("length", [0, 1, 5, 15, 16, 17, 31, 32, 100, 2 ** 31 - 1, -3])
+def test_store_work_covers_each_token_once(ix, n, length):
+    """The tokens' positions, cut into blocks of 16: each position is in one
+    block's range, also positions in front of 0."""
+    o, r = (ctypes.c_longlong * 5)(), (ctypes.c_int * 2)()
+    ix.s_store_work(7, 7 + n, length, 1000, 3, o)
+    assert o[0] == n and o[3] == length - n and o[4] == 3 * o[2]
+    seen = []
+    for block in range(o[1], o[1] + o[2]):
+        ix.s_block_range(7, 7 + n, length, 1000, block, r)
+        assert 0 <= r[0] < r[1] <= 16
+        seen += [block * 16 + t for t in range(r[0], r[1])]
+    assert seen == list(range(length - n, length))
+    assert o[2] <= n // 16 + 2
 
 
 def batches():

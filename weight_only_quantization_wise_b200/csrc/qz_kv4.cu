@@ -19,191 +19,475 @@ using namespace kv4;
 constexpr unsigned kErrIndex = 2u;     // bit of the device error word: bad page or position
 
 // ---------------------------------------------------------------------------
-// append: one warp per (token, key head)
+// append and read
 // ---------------------------------------------------------------------------
+// A unit is one record's worth of tokens: 16 positions (or the part of them
+// that is the call's) of one head.  A warp stages the tokens' 16 x D bf16
+// values and the record in shared memory, so that global memory is read and
+// written in whole rows and whole records; in between a lane works on 64
+// consecutive values of one token ("chunk"), which hold whole groups (or half
+// a group of 128) and whole 32-bit words of K and 16-bit units of V.
 struct StoreArgs {
-    const uint16_t *k, *v;             // append: input; read: unused
-    uint16_t *k_out, *v_out;           // read
+    const uint16_t *k, *v;             // append: input
+    uint16_t *k_out, *v_out;           // read: output
     int64_t k_stride, v_stride;        // elements between tokens
     uint8_t *cache;
     const int32_t *page_table, *kv_lens, *cu;
-    int64_t T, B, max_pages, num_pages;
-    int kv_heads, page_size;
+    int64_t max_pages, num_pages;
+    int T, B, kv_heads, page_blocks;
     unsigned int *err_word;
 };
 
-constexpr int kStoreWarps = 8;
-
-// Token t's place: its sequence's page-table row and position, false for a
-// token behind the last sequence.
-__device__ __forceinline__ bool locate(const StoreArgs &p, int64_t t, int64_t &b, int64_t &pos) {
-    b = find_sequence(p.cu, p.B, t);
-    if (b < 0) return false;
-    pos = (int64_t)p.kv_lens[b] - ((int64_t)p.cu[b + 1] - t);
-    return true;
-}
-
-// Scale, zero and codes as qz_quantize_pack forms them (qz.h: range widened
-// to 0, S = (max - min) / 15 in fp32 stored as bf16 rounded up, 0 -> 1).
-// code = clamp(round(x / S + Z)): with r = 1/S rounded, fma(x, r, Z + 192)
-// lies on the same side of every half-way point as x / S + Z (bf16 x and S
-// keep x / S + Z at least 2^-10 from a half-way point it does not hit; the
-// argument is written out at chunk_codes in qz_quantize.cu), and adding
-// 1.5 2^23 - 192 rounds half to even into the low mantissa bits.
-__device__ __forceinline__ uint32_t code4(float x, float s, float r, float z) {
-    if (!(r < __int_as_float(0x7F800000))) {        // 1/S overflows: IEEE division
-        const int q = (int)rintf(__fadd_rn(__fdiv_rn(x, s), z));
-        return (uint32_t)min(max(q, 0), 15);
-    }
-    const float y = __fmaf_rn(x, r, __fadd_rn(z, 192.0f));
-    const uint32_t b = __float_as_uint(__fadd_rn(y, 12582912.0f - 192.0f));
-    return min(b, 0x4B40000Fu) & 15u;
-}
+constexpr int kStoreWarps = 4;
+constexpr int kStoreThreads = 32 * kStoreWarps;
+constexpr int kChunkPitch = 144;       // bytes of a staged chunk: 64 bf16, padded against bank conflicts
 
 template <int D, int G>
-__device__ __forceinline__ void quantize_head(const uint16_t *src, int lane, uint8_t *codes,
-                                              uint16_t *scales, uint8_t *zeros) {
-    constexpr int V = D / 32;                        // values per lane, consecutive
-    constexpr int LPG = G / V;                       // lanes per group
-    float x[V];
-    if constexpr (V == 2) {
-        const uint32_t w = reinterpret_cast<const uint32_t *>(src)[lane];
-        x[0] = dev::bf16_lo(w); x[1] = dev::bf16_hi(w);
-    } else if constexpr (V == 4) {
-        const uint2 w = reinterpret_cast<const uint2 *>(src)[lane];
-        x[0] = dev::bf16_lo(w.x); x[1] = dev::bf16_hi(w.x);
-        x[2] = dev::bf16_lo(w.y); x[3] = dev::bf16_hi(w.y);
-    } else {
-        const uint4 w = reinterpret_cast<const uint4 *>(src)[lane];
-        x[0] = dev::bf16_lo(w.x); x[1] = dev::bf16_hi(w.x);
-        x[2] = dev::bf16_lo(w.y); x[3] = dev::bf16_hi(w.y);
-        x[4] = dev::bf16_lo(w.z); x[5] = dev::bf16_hi(w.z);
-        x[6] = dev::bf16_lo(w.w); x[7] = dev::bf16_hi(w.w);
-    }
-    float lo = 0.0f, hi = 0.0f;
+struct StoreLayout {
+    static constexpr int NG = D / G;
+    static constexpr int chunks = D / 64;                   // of a token
+    static constexpr int rec = (int)record_bytes(D, G);
+    static constexpr int tile = 16 * chunks * kChunkPitch;  // one tensor's staged tokens
+    static constexpr int per_warp = 2 * tile + rec;         // K, V, record
+};
+
+// Adds up the sequences' units and finds where warp `gw` of `warps` starts:
+// calls unit(b, work, index in the sequence) for each unit of its range.
+template <typename F>
+__device__ __forceinline__ void for_units(const StoreArgs &p, F unit) {
+    __shared__ int64_t pre[kStoreThreads + 1], warp_sum[kStoreWarps];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    auto work_of = [&](int b) {
+        return store_work(p.cu[b], p.cu[b + 1], p.kv_lens[b], p.T, p.kv_heads);
+    };
+    const int per = (p.B + kStoreThreads - 1) / kStoreThreads;
+    int64_t scan = 0;
+    for (int i = 0; i < per; ++i)
+        if (tid * per + i < p.B) scan += work_of(tid * per + i).units;
 #pragma unroll
-    for (int i = 0; i < V; ++i) { lo = fminf(lo, x[i]); hi = fmaxf(hi, x[i]); }
-#pragma unroll
-    for (int o = 1; o < LPG; o <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, scan, o);
+        if (lane >= o) scan += v;
     }
-    float s = __fdiv_rn(__fsub_rn(hi, lo), 15.0f);
+    if (lane == 31) warp_sum[warp] = scan;
+    __syncthreads();
+    int64_t before = 0, units = 0;
+#pragma unroll
+    for (int w = 0; w < kStoreWarps; ++w) {
+        if (w < warp) before += warp_sum[w];
+        units += warp_sum[w];
+    }
+    pre[tid + 1] = before + scan;
+    if (tid == 0) pre[0] = 0;
+    __syncthreads();
+    const int64_t warps = (int64_t)gridDim.x * kStoreWarps;
+    const int64_t quota = quotient(units + warps - 1, warps);
+    // consecutive units go to different CTAs while there are few
+    int64_t u = ((int64_t)warp * gridDim.x + blockIdx.x) * quota;
+    const int64_t end = min(u + quota, units);
+    if (u >= end) return;
+    int lo = 0;
+    for (int i = lane; i < kStoreThreads; i += 32)
+        if (pre[i] <= u) lo = i;
+    lo = __reduce_max_sync(0xFFFFFFFFu, lo);
+    int b = lo * per;
+    int64_t begin = pre[lo];
+    StoreWork w = work_of(b);
+    while (u < end) {
+        while (u >= begin + w.units) {
+            begin += w.units;
+            w = work_of(++b);
+        }
+        unit(b, w, u - begin);
+        ++u;
+    }
+}
+
+// Codes of 8 values (word: value i in nibble i), clamp(round(x / S + Z)) as
+// qz_quantize_pack forms them: with r = 1/S rounded, fma(x, r, Z + 192) lies on
+// the same side of every half-way point as x / S + Z (bf16 x and S keep x / S +
+// Z at least 2^-10 from a half-way point it does not hit; the argument is
+// written out at chunk_codes in qz_quantize.cu), and adding 1.5 2^23 - 192
+// rounds half to even into the low mantissa bits.  Two values per fma and add.
+__device__ __forceinline__ uint32_t codes8(const uint4 &x, float r, float zc) {
+    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+    uint32_t pair[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t a, c;
+        asm("{\n\t.reg .b64 xx, rr, zz, kk, yy;\n\t"
+            "mov.b64 xx, {%2, %3};\n\tmov.b64 rr, {%4, %4};\n\t"
+            "mov.b64 zz, {%5, %5};\n\tmov.b64 kk, {%6, %6};\n\t"
+            "fma.rn.f32x2 yy, xx, rr, zz;\n\tadd.rn.f32x2 yy, yy, kk;\n\t"
+            "mov.b64 {%0, %1}, yy;\n\t}"
+            : "=r"(a), "=r"(c)
+            : "r"(u[i] << 16), "r"(u[i] & 0xFFFF0000u), "r"(__float_as_uint(r)),
+              "r"(__float_as_uint(zc)), "r"(__float_as_uint(12582912.0f - 192.0f)));
+        a = min(a, 0x4B40000Fu);
+        c = min(c, 0x4B40000Fu);
+        pair[i] = dev::and_or<0x0Fu>(a, c << 4);            // byte 0: both codes
+    }
+    return dev::prmt(dev::prmt(pair[0], pair[1], 0x0040u), dev::prmt(pair[2], pair[3], 0x0040u),
+                     0x5410u);
+}
+// The same with the IEEE division, for scales whose inverse overflows.
+__device__ __forceinline__ uint32_t code4_exact(float x, float s, float z) {
+    const int q = (int)rintf(__fadd_rn(__fdiv_rn(x, s), z));
+    return (uint32_t)min(max(q, 0), 15);
+}
+__device__ __noinline__ uint32_t codes8_exact(uint4 x, float s, float z) {
+    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+    uint32_t word = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        word |= code4_exact(dev::bf16_lo(u[i]), s, z) << (8 * i) |
+                code4_exact(dev::bf16_hi(u[i]), s, z) << (8 * i + 4);
+    return word;
+}
+
+// Transposes 4 x 8 nibbles: words a, b, c, d of 8 nibbles -> units g = 0..7 of
+// four nibbles (a_g, b_g, c_g, d_g); out[0] = units 0, 2, out[1] = 4, 6,
+// out[2] = 1, 3, out[3] = 5, 7 (low half, high half).
+__device__ __forceinline__ void nibbles_to_units(uint32_t a, uint32_t b, uint32_t c, uint32_t d,
+                                                 uint32_t (&out)[4]) {
+    constexpr uint32_t m = 0x0F0F0F0Fu;
+    const uint32_t e0 = (a & m) | ((b & m) << 4), e1 = ((a >> 4) & m) | (b & ~m);
+    const uint32_t f0 = (c & m) | ((d & m) << 4), f1 = ((c >> 4) & m) | (d & ~m);
+    out[0] = dev::prmt(e0, f0, 0x5140u);
+    out[1] = dev::prmt(e0, f0, 0x7362u);
+    out[2] = dev::prmt(e1, f1, 0x5140u);
+    out[3] = dev::prmt(e1, f1, 0x7362u);
+}
+// The inverse: units u[0..7] (low halves) -> words a, b, c, d.
+__device__ __forceinline__ void units_to_nibbles(const uint32_t (&u)[8], uint32_t &a, uint32_t &b,
+                                                 uint32_t &c, uint32_t &d) {
+    constexpr uint32_t m = 0x0F0F0F0Fu;
+    const uint32_t p0 = dev::prmt(u[0], u[2], 0x5140u), p1 = dev::prmt(u[4], u[6], 0x5140u);
+    const uint32_t q0 = dev::prmt(u[1], u[3], 0x5140u), q1 = dev::prmt(u[5], u[7], 0x5140u);
+    const uint32_t e0 = dev::prmt(p0, p1, 0x5410u), f0 = dev::prmt(p0, p1, 0x7632u);
+    const uint32_t e1 = dev::prmt(q0, q1, 0x5410u), f1 = dev::prmt(q0, q1, 0x7632u);
+    a = (e0 & m) | ((e1 & m) << 4);
+    b = ((e0 >> 4) & m) | (e1 & ~m);
+    c = (f0 & m) | ((f1 & m) << 4);
+    d = ((f0 >> 4) & m) | (f1 & ~m);
+}
+__device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Scale (bf16 bits) and zero of a group with the 0-extended range [lo, hi]
+// (qz.h: S = (max - min) / 15 in fp32 stored as bf16 rounded up, 0 -> 1).
+__device__ __forceinline__ uint32_t group_scale(float lo, float hi, float &s, float &z) {
+    s = __fdiv_rn(__fsub_rn(hi, lo), 15.0f);
     if (s == 0.0f) s = 1.0f;
     const uint32_t sb = dev::bf16_round_up_bits(s);
     s = __uint_as_float(sb << 16);
-    const float z = -rintf(__fdiv_rn(lo, s));
-    const float r = __frcp_rn(s);
-#pragma unroll
-    for (int i = 0; i < V; ++i) codes[lane * V + i] = (uint8_t)code4(x[i], s, r, z);
-    if ((lane & (LPG - 1)) == 0) {
-        scales[16 * (lane / LPG)] = (uint16_t)sb;
-        zeros[16 * (lane / LPG)] = (uint8_t)(int)z;
-    }
+    z = -rintf(__fdiv_rn(lo, s));
+    return sb;
 }
 
+// One token of one head into its record `dst`; a lane holds D / 32 consecutive
+// values of the keys, then of the values.  `buf`: D bytes of the warp's own.
 template <int D, int G>
-__global__ void __launch_bounds__(32 * kStoreWarps) kv4_append_kernel(const StoreArgs p) {
-    constexpr int NG = D / G;
-    __shared__ __align__(16) uint8_t buf[kStoreWarps][D];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int64_t item = (int64_t)blockIdx.x * kStoreWarps + w;
-    if (item >= p.T * p.kv_heads) return;
-    const int64_t t = item / p.kv_heads;
-    const int h = (int)(item - t * p.kv_heads);
-    int64_t b, pos;
-    if (!locate(p, t, b, pos)) return;
-    int64_t rec = -1;
-    if (pos >= 0)
-        rec = record_index(p.page_table + b * p.max_pages, p.max_pages, p.num_pages, p.kv_heads,
-                           h, p.page_size / kBlock, (int)(pos / kBlock));
-    if (rec < 0) {
-        if (lane == 0) atomicOr(p.err_word, kErrIndex);
-        return;
+__device__ __forceinline__ void append_token(const uint16_t *k, const uint16_t *v, int t, uint8_t *dst,
+                                             uint8_t *buf, int lane) {
+    constexpr int NG = D / G, V = D / 32, LPG = G / V;       // LPG lanes per group
+    uint32_t w[2][V / 2];
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        const uint32_t *src = reinterpret_cast<const uint32_t *>(which ? v : k) + lane * (V / 2);
+        if constexpr (V == 2) {
+            w[which][0] = __ldg(src);
+        } else if constexpr (V == 4) {
+            const uint2 x = __ldg(reinterpret_cast<const uint2 *>(src));
+            w[which][0] = x.x; w[which][1] = x.y;
+        } else {
+            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(src));
+            w[which][0] = x.x; w[which][1] = x.y; w[which][2] = x.z; w[which][3] = x.w;
+        }
     }
-    uint8_t *r = p.cache + rec * record_bytes(D, G);
-    const int tk = (int)(pos % kBlock);
-    uint8_t *c = buf[w];
-    quantize_head<D, G>(p.k + t * p.k_stride + (int64_t)h * D, lane, c,
-                        reinterpret_cast<uint16_t *>(r + k_scales_off(D)) + tk,
-                        r + k_zeros_off(D, NG) + tk);
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        float mn = 0.0f, mx = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            mn = fminf(mn, fminf(dev::bf16_lo(w[which][i]), dev::bf16_hi(w[which][i])));
+            mx = fmaxf(mx, fmaxf(dev::bf16_lo(w[which][i]), dev::bf16_hi(w[which][i])));
+        }
+#pragma unroll
+        for (int o = 1; o < LPG; o <<= 1) {
+            mn = fminf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, o));
+            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+        }
+        float s, z;
+        const uint32_t sb = group_scale(mn, mx, s, z);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            buf[which * D + lane * V + 2 * i] = (uint8_t)code4_exact(dev::bf16_lo(w[which][i]), s, z);
+            buf[which * D + lane * V + 2 * i + 1] =
+                (uint8_t)code4_exact(dev::bf16_hi(w[which][i]), s, z);
+        }
+        if ((lane & (LPG - 1)) == 0) {
+            const int so = 16 * (lane / LPG) + t;
+            *reinterpret_cast<uint16_t *>(dst + (which ? v_scales_off(D, NG) : k_scales_off(D)) +
+                                          2 * so) = (uint16_t)sb;
+            dst[(which ? v_zeros_off(D, NG) : k_zeros_off(D, NG)) + so] = (uint8_t)(int)z;
+        }
+    }
     __syncwarp();
     if (lane < D / 8) {
-        const uint2 v = reinterpret_cast<const uint2 *>(c)[lane];
-        uint32_t lo = v.x | (v.x >> 4), hi = v.y | (v.y >> 4);   // nibble pairs in bytes 0 and 2
-        lo = (lo & 0xFFu) | ((lo >> 8) & 0xFF00u);
-        hi = (hi & 0xFFu) | ((hi >> 8) & 0xFF00u);
-        *reinterpret_cast<uint32_t *>(r + k_codes_off() + k_word_byte(D, tk, lane)) =
-            lo | (hi << 16);
+        const uint2 x = reinterpret_cast<const uint2 *>(buf)[lane];
+        const uint32_t lo = x.x | (x.x >> 4), hi = x.y | (x.y >> 4);   // pairs in bytes 0 and 2
+        *reinterpret_cast<uint32_t *>(dst + k_codes_off() + k_word_byte(D, t, lane)) =
+            dev::prmt(lo, hi, 0x6420u);
     }
-    __syncwarp();
-    quantize_head<D, G>(p.v + t * p.v_stride + (int64_t)h * D, lane, c,
-                        reinterpret_cast<uint16_t *>(r + v_scales_off(D, NG)) + tk,
-                        r + v_zeros_off(D, NG) + tk);
-    __syncwarp();
     for (int u = lane; u < D / 4; u += 32) {
         const int gid = u & 7, hi = (u >> 3) & 1, wi = u >> 4;
-        uint32_t v = 0;
+        uint32_t x = 0;
 #pragma unroll
-        for (int n = 0; n < 4; ++n) v |= (uint32_t)c[64 * wi + 16 * n + 8 * hi + gid] << (4 * n);
-        *reinterpret_cast<uint16_t *>(r + v_codes_off(D) + v_unit_byte(D, tk, wi, hi, gid)) =
-            (uint16_t)v;
+        for (int n = 0; n < 4; ++n) x |= (uint32_t)buf[D + 64 * wi + 16 * n + 8 * hi + gid] << (4 * n);
+        *reinterpret_cast<uint16_t *>(dst + v_codes_off(D) + v_unit_byte(D, t, wi, hi, gid)) =
+            (uint16_t)x;
     }
+    __syncwarp();
 }
 
-// ---------------------------------------------------------------------------
-// read: one warp per (token, key head); lane l < D / 8 gives d = 8 l .. 8 l + 7
-// ---------------------------------------------------------------------------
 template <int D, int G>
-__global__ void __launch_bounds__(32 * kStoreWarps) kv4_read_kernel(const StoreArgs p) {
-    constexpr int NG = D / G;
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int64_t item = (int64_t)blockIdx.x * kStoreWarps + w;
-    if (item >= p.T * p.kv_heads) return;
-    const int64_t t = item / p.kv_heads;
-    const int h = (int)(item - t * p.kv_heads);
-    int64_t b, pos;
-    if (!locate(p, t, b, pos)) return;
-    if (lane >= D / 8) return;
-    uint16_t *ko = p.k_out + item * D + 8 * lane, *vo = p.v_out + item * D + 8 * lane;
-    int64_t rec = -1;
-    if (pos >= 0)
-        rec = record_index(p.page_table + b * p.max_pages, p.max_pages, p.num_pages, p.kv_heads,
-                           h, p.page_size / kBlock, (int)(pos / kBlock));
-    if (rec < 0) {
-        *reinterpret_cast<uint4 *>(ko) = make_uint4(0u, 0u, 0u, 0u);
-        *reinterpret_cast<uint4 *>(vo) = make_uint4(0u, 0u, 0u, 0u);
-        if (lane == 0) atomicOr(p.err_word, kErrIndex);
-        return;
-    }
-    const uint8_t *r = p.cache + rec * record_bytes(D, G);
-    const int tk = (int)(pos % kBlock);
-    const int grp = 8 * lane / G;
-    uint32_t kc = *reinterpret_cast<const uint32_t *>(r + k_word_byte(D, tk, lane));
-    uint32_t vc = 0;
-    const int wi = lane >> 3, n = (lane >> 1) & 3, hi = lane & 1;
+__global__ void __launch_bounds__(kStoreThreads) kv4_append_kernel(const StoreArgs p) {
+    using L = StoreLayout<D, G>;
+    constexpr int NG = L::NG, CH = L::chunks, W8 = D / 8;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int lane = threadIdx.x & 31;
+    uint8_t *tile = smem + (threadIdx.x >> 5) * L::per_warp, *rec = tile + 2 * L::tile;
+    for_units(p, [&](int b, const StoreWork &w, int64_t index) {
+        const int i = (int)quotient(index, p.kv_heads), h = (int)(index - (int64_t)i * p.kv_heads);
+        const int block = w.block0 + i;
+        const int lo = block_lo(w, block), hi = block_hi(w, block);
+        const int64_t r = record_index(p.page_table + (int64_t)b * p.max_pages, p.max_pages,
+                                       p.num_pages, p.kv_heads, h, p.page_blocks, block);
+        if (r < 0) {
+            if (lane == 0) atomicOr(p.err_word, kErrIndex);
+            return;
+        }
+        const int64_t row0 = p.cu[b] + ((int64_t)block * kBlock - w.first);   // of token 0
+        uint8_t *dst = p.cache + r * L::rec;
+        const int end = (int)min((int64_t)hi, p.T - row0);
+        if (end - lo <= 2) {
+            // ---- a token or two (decoding): a lane takes D / 32 values ----
+            for (int t = lo; t < end; ++t)
+                append_token<D, G>(p.k + (row0 + t) * p.k_stride + (int64_t)h * D,
+                                   p.v + (row0 + t) * p.v_stride + (int64_t)h * D, t, dst, rec, lane);
+            return;
+        }
+        // ---- the tokens' values, 16 bytes per lane and load ----
+        uint4 v[2][16 * W8 / 32];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t u = *reinterpret_cast<const uint16_t *>(r + v_codes_off(D) +
-                                                               v_unit_byte(D, tk, wi, hi, i));
-        vc |= ((u >> (4 * n)) & 15u) << (4 * i);
-    }
-    const int so = 16 * grp + tk;
-    const float ks = __uint_as_float(
-        (uint32_t)reinterpret_cast<const uint16_t *>(r + k_scales_off(D))[so] << 16);
-    const float vs = __uint_as_float(
-        (uint32_t)reinterpret_cast<const uint16_t *>(r + v_scales_off(D, NG))[so] << 16);
-    const int kz = r[k_zeros_off(D, NG) + so], vz = r[v_zeros_off(D, NG) + so];
-    uint32_t ko2[4], vo2[4];
+        for (int t2 = 0; t2 < 2; ++t2)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int a = (int)((kc >> (8 * i)) & 15u) - kz, c = (int)((kc >> (8 * i + 4)) & 15u) - kz;
-        const int e = (int)((vc >> (8 * i)) & 15u) - vz, f = (int)((vc >> (8 * i + 4)) & 15u) - vz;
-        ko2[i] = dev::pack_bf16x2(ks * (float)a, ks * (float)c);
-        vo2[i] = dev::pack_bf16x2(vs * (float)e, vs * (float)f);
-    }
-    *reinterpret_cast<uint4 *>(ko) = make_uint4(ko2[0], ko2[1], ko2[2], ko2[3]);
-    *reinterpret_cast<uint4 *>(vo) = make_uint4(vo2[0], vo2[1], vo2[2], vo2[3]);
+            for (int x = 0; x < 16 * W8 / 32; ++x) {
+                const int e = x * 32 + lane, t = e / W8;
+                v[t2][x] = t >= lo && t < end
+                               ? __ldg(reinterpret_cast<const uint4 *>(
+                                     (t2 ? p.v : p.k) + (int64_t)h * D +
+                                     (row0 + t) * (t2 ? p.v_stride : p.k_stride) + 8 * (e % W8)))
+                               : make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+        for (int t2 = 0; t2 < 2; ++t2)
+#pragma unroll
+            for (int x = 0; x < 16 * W8 / 32; ++x) {
+                const int e = x * 32 + lane, t = e / W8, c8 = e % W8;
+                *reinterpret_cast<uint4 *>(tile + t2 * L::tile + (t * CH + c8 / 8) * kChunkPitch +
+                                           16 * (c8 % 8)) = v[t2][x];
+            }
+        __syncwarp();
+        // ---- chunks: the keys', then the values' ----
+#pragma unroll
+        for (int pass = 0; pass < CH; ++pass) {
+            const int id = pass * 32 + lane, which = id / (16 * CH);
+            const int t = id % (16 * CH) / CH, wi = id % CH;
+            const uint8_t *src = tile + which * L::tile + (t * CH + wi) * kChunkPitch;
+            uint4 x[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) x[q] = *reinterpret_cast<const uint4 *>(src + 16 * q);
+            constexpr int GC = G < 64 ? 64 / G : 1;         // groups of a chunk
+            uint32_t codes[8];                              // word q: d = 8 q .. 8 q + 7
+#pragma unroll
+            for (int gc = 0; gc < GC; ++gc) {
+                uint32_t mn2 = 0, mx2 = 0;                  // pairs, from 0
+#pragma unroll
+                for (int q = gc * (8 / GC); q < (gc + 1) * (8 / GC); ++q) {
+                    mn2 = min_bf16x2(mn2, min_bf16x2(min_bf16x2(x[q].x, x[q].y), min_bf16x2(x[q].z, x[q].w)));
+                    mx2 = max_bf16x2(mx2, max_bf16x2(max_bf16x2(x[q].x, x[q].y), max_bf16x2(x[q].z, x[q].w)));
+                }
+                float mn = fminf(dev::bf16_lo(mn2), dev::bf16_hi(mn2));
+                float mx = fmaxf(dev::bf16_lo(mx2), dev::bf16_hi(mx2));
+                if constexpr (G == 128) {
+                    mn = fminf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, 1));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+                }
+                float s, z;
+                const uint32_t sb = group_scale(mn, mx, s, z);
+                const float inv = __frcp_rn(s), zc = __fadd_rn(z, 192.0f);
+                if (inv < __int_as_float(0x7F800000)) {
+#pragma unroll
+                    for (int q = gc * (8 / GC); q < (gc + 1) * (8 / GC); ++q)
+                        codes[q] = codes8(x[q], inv, zc);
+                } else {
+#pragma unroll
+                    for (int q = gc * (8 / GC); q < (gc + 1) * (8 / GC); ++q)
+                        codes[q] = codes8_exact(x[q], s, z);
+                }
+                const int so = 16 * (G == 128 ? wi >> 1 : wi * GC + gc) + t;
+                if (G != 128 || (wi & 1) == 0) {
+                    *reinterpret_cast<uint16_t *>(
+                        rec + (which ? v_scales_off(D, NG) : k_scales_off(D)) + 2 * so) = (uint16_t)sb;
+                    rec[(which ? v_zeros_off(D, NG) : k_zeros_off(D, NG)) + so] = (uint8_t)(int)z;
+                }
+            }
+            if (which == 0) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    *reinterpret_cast<uint32_t *>(rec + k_word_byte(D, t, 8 * wi + q)) = codes[q];
+            } else {
+                // unit (uh, g): codes d = 16 n + 8 uh + g, n = 0..3
+#pragma unroll
+                for (int uh = 0; uh < 2; ++uh) {
+                    uint32_t u[4];
+                    nibbles_to_units(codes[uh], codes[2 + uh], codes[4 + uh], codes[6 + uh], u);
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const int g8 = 4 * (y & 1) + (y >> 1);         // and g8 + 2
+                        *reinterpret_cast<uint16_t *>(rec + v_codes_off(D) +
+                                                      v_unit_byte(D, t, wi, uh, g8)) = (uint16_t)u[y];
+                        *reinterpret_cast<uint16_t *>(rec + v_codes_off(D) +
+                                                      v_unit_byte(D, t, wi, uh, g8 + 2)) =
+                            (uint16_t)(u[y] >> 16);
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        // ---- out: the whole record, or the bytes of the call's tokens alone ----
+        if (lo == 0 && end == kBlock) {
+            for (int e = lane; e < L::rec / 16; e += 32)
+                reinterpret_cast<uint4 *>(dst)[e] = reinterpret_cast<const uint4 *>(rec)[e];
+        } else {
+            for (int e = lane; e < 16 * W8; e += 32) {
+                const int t = e / W8, o = k_word_byte(D, t, e % W8);
+                if (t >= lo && t < end)
+                    *reinterpret_cast<uint32_t *>(dst + o) = *reinterpret_cast<uint32_t *>(rec + o);
+            }
+            for (int e = lane; e < 16 * (D / 4); e += 32) {
+                const int t = e / (D / 4), u = e % (D / 4);
+                const int o = v_codes_off(D) + v_unit_byte(D, t, u >> 4, (u >> 3) & 1, u & 7);
+                if (t >= lo && t < end)
+                    *reinterpret_cast<uint16_t *>(dst + o) = *reinterpret_cast<uint16_t *>(rec + o);
+            }
+            for (int e = lane; e < 2 * NG * 16; e += 32) {   // K groups, then V groups
+                const int t = e & 15;
+                if (t < lo || t >= end) continue;
+                const int o = k_scales_off(D) + 2 * e, oz = k_zeros_off(D, NG) + e;
+                *reinterpret_cast<uint16_t *>(dst + o) = *reinterpret_cast<uint16_t *>(rec + o);
+                dst[oz] = rec[oz];
+            }
+        }
+        __syncwarp();
+    });
+}
+
+template <int D, int G>
+__global__ void __launch_bounds__(kStoreThreads) kv4_read_kernel(const StoreArgs p) {
+    using L = StoreLayout<D, G>;
+    constexpr int NG = L::NG, CH = L::chunks, W8 = D / 8;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int lane = threadIdx.x & 31;
+    uint8_t *tile = smem + (threadIdx.x >> 5) * L::per_warp, *rec = tile + 2 * L::tile;
+    for_units(p, [&](int b, const StoreWork &w, int64_t index) {
+        const int i = (int)quotient(index, p.kv_heads), h = (int)(index - (int64_t)i * p.kv_heads);
+        const int block = w.block0 + i;
+        const int lo = block_lo(w, block), hi = block_hi(w, block);
+        const int64_t r = record_index(p.page_table + (int64_t)b * p.max_pages, p.max_pages,
+                                       p.num_pages, p.kv_heads, h, p.page_blocks, block);
+        const int64_t row0 = p.cu[b] + ((int64_t)block * kBlock - w.first);   // of token 0
+        if (r < 0) {
+            if (lane == 0) atomicOr(p.err_word, kErrIndex);
+        } else {
+            const uint4 *src = reinterpret_cast<const uint4 *>(p.cache + r * L::rec);
+            constexpr int NV = L::rec / 16;
+            uint4 v[(NV + 31) / 32];
+#pragma unroll
+            for (int x = 0; x < (NV + 31) / 32; ++x)
+                if (x * 32 + lane < NV) v[x] = __ldg(src + x * 32 + lane);
+#pragma unroll
+            for (int x = 0; x < (NV + 31) / 32; ++x)
+                if (x * 32 + lane < NV) reinterpret_cast<uint4 *>(rec)[x * 32 + lane] = v[x];
+        }
+        __syncwarp();
+#pragma unroll
+        for (int pass = 0; pass < CH; ++pass) {
+            const int id = pass * 32 + lane, which = id / (16 * CH);
+            const int t = id % (16 * CH) / CH, wi = id % CH;
+            uint32_t codes[8];                              // word q: d = 8 q .. 8 q + 7
+            if (which == 0) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    codes[q] = *reinterpret_cast<const uint32_t *>(rec + k_word_byte(D, t, 8 * wi + q));
+            } else {
+#pragma unroll
+                for (int uh = 0; uh < 2; ++uh) {
+                    uint32_t u[8];
+#pragma unroll
+                    for (int g8 = 0; g8 < 8; ++g8)
+                        u[g8] = *reinterpret_cast<const uint16_t *>(
+                            rec + v_codes_off(D) + v_unit_byte(D, t, wi, uh, g8));
+                    units_to_nibbles(u, codes[uh], codes[2 + uh], codes[4 + uh], codes[6 + uh]);
+                }
+            }
+            uint8_t *dst = tile + which * L::tile + (t * CH + wi) * kChunkPitch;
+            constexpr int GC = G < 64 ? 64 / G : 1;         // groups of a chunk
+#pragma unroll
+            for (int gc = 0; gc < GC; ++gc) {
+                const int so = 16 * ((64 * wi + (64 / GC) * gc) / G) + t;
+                uint32_t s2 = *reinterpret_cast<const uint16_t *>(
+                    rec + (which ? v_scales_off(D, NG) : k_scales_off(D)) + 2 * so);
+                uint32_t z2 = rec[(which ? v_zeros_off(D, NG) : k_zeros_off(D, NG)) + so];
+                if (r < 0) s2 = z2 = 0;
+                s2 *= 0x00010001u;                          // (S, S)
+                z2 = (0x4300u + z2) * 0x00010001u;          // bf16(128 + Z) twice
+#pragma unroll
+                for (int q = gc * (8 / GC); q < (gc + 1) * (8 / GC); ++q) {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)             // bf16(S (q - Z)), rounded once
+                        o[y] = dequant_pair_nat(codes[q], codes[q] >> 4, y, s2, z2);
+                    *reinterpret_cast<uint4 *>(dst + 16 * q) = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+            }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int t2 = 0; t2 < 2; ++t2) {
+            uint16_t *out = (t2 ? p.v_out : p.k_out) + (int64_t)h * D;
+#pragma unroll
+            for (int x = 0; x < 16 * W8 / 32; ++x) {
+                const int e = x * 32 + lane, t = e / W8, c8 = e % W8;
+                const int64_t row = row0 + t;
+                if (t >= lo && t < hi && row < p.T)
+                    *reinterpret_cast<uint4 *>(out + row * (int64_t)p.kv_heads * D + 8 * c8) =
+                        *reinterpret_cast<const uint4 *>(tile + t2 * L::tile +
+                                                         (t * CH + c8 / 8) * kChunkPitch + 16 * (c8 % 8));
+            }
+        }
+        __syncwarp();
+    });
 }
 
 // ---------------------------------------------------------------------------
@@ -1118,18 +1402,42 @@ qz_status dispatch(int64_t D, int64_t G, A &&...a) {
     return G == 64 ? Op<256, 64>::go(a...) : Op<256, 128>::go(a...);
 }
 
+// As many CTAs as an SM's shared memory holds, and no more than there can be
+// warps with work (a call's tokens lie in at most T / 16 + 2 B blocks).
+template <typename K>
+qz_status launch_store(K kernel, int per_warp, const StoreArgs &p, DeviceOnce &once,
+                       cudaStream_t st) {
+    const int smem = per_warp * kStoreWarps;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return QZ_ERR_CUDA;
+    }
+    if (once.run(dev, [&] {
+            cudaError_t e =
+                cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+            return e;
+        }) != cudaSuccess)
+        return QZ_ERR_CUDA;
+    const int64_t most = ceil_div(((int64_t)p.T / kBlock + 2 * (int64_t)p.B) * p.kv_heads, kStoreWarps);
+    const int64_t fit = (int64_t)device_sm_count() * (220 * 1024 / (smem + 4096));
+    kernel<<<(unsigned)(most < fit ? most : fit), kStoreThreads, smem, st>>>(p);
+    return launch_status();
+}
 template <int D, int G>
 struct Append {
-    static qz_status go(const StoreArgs &p, unsigned grid, cudaStream_t st) {
-        kv4_append_kernel<D, G><<<grid, 32 * kStoreWarps, 0, st>>>(p);
-        return launch_status();
+    static qz_status go(const StoreArgs &p, cudaStream_t st) {
+        static DeviceOnce once;
+        return launch_store(kv4_append_kernel<D, G>, StoreLayout<D, G>::per_warp, p, once, st);
     }
 };
 template <int D, int G>
 struct Read {
-    static qz_status go(const StoreArgs &p, unsigned grid, cudaStream_t st) {
-        kv4_read_kernel<D, G><<<grid, 32 * kStoreWarps, 0, st>>>(p);
-        return launch_status();
+    static qz_status go(const StoreArgs &p, cudaStream_t st) {
+        static DeviceOnce once;
+        return launch_store(kv4_read_kernel<D, G>, StoreLayout<D, G>::per_warp, p, once, st);
     }
 };
 template <int D, int G>
@@ -1145,9 +1453,9 @@ StoreArgs store_args(const Kv4Cache &c) {
     p.page_table = static_cast<const int32_t *>(c.page_table);
     p.kv_lens = static_cast<const int32_t *>(c.kv_lens);
     p.cu = static_cast<const int32_t *>(c.cu);
-    p.T = c.T; p.B = c.B;
+    p.T = (int)c.T; p.B = (int)c.B;
     p.max_pages = c.max_pages; p.num_pages = c.num_pages;
-    p.kv_heads = (int)c.kv_heads; p.page_size = (int)c.page_size;
+    p.kv_heads = (int)c.kv_heads; p.page_blocks = (int)(c.page_size / kBlock);
     p.err_word = device_error_word();
     return p;
 }
@@ -1174,8 +1482,7 @@ qz_status launch_kv4_append(const Kv4Cache &c, const void *k, const void *v, int
     p.v = static_cast<const uint16_t *>(v);
     p.k_stride = k_stride;
     p.v_stride = v_stride;
-    return dispatch<Append>(c.head_dim, c.group_size, p,
-                            (unsigned)ceil_div(c.T * c.kv_heads, kStoreWarps), st);
+    return dispatch<Append>(c.head_dim, c.group_size, p, st);
 }
 
 qz_status launch_kv4_read(const Kv4Cache &c, void *k, void *v, cudaStream_t st) {
@@ -1183,8 +1490,7 @@ qz_status launch_kv4_read(const Kv4Cache &c, void *k, void *v, cudaStream_t st) 
     if (p.err_word == nullptr) return QZ_ERR_CUDA;
     p.k_out = static_cast<uint16_t *>(k);
     p.v_out = static_cast<uint16_t *>(v);
-    return dispatch<Read>(c.head_dim, c.group_size, p,
-                          (unsigned)ceil_div(c.T * c.kv_heads, kStoreWarps), st);
+    return dispatch<Read>(c.head_dim, c.group_size, p, st);
 }
 
 qz_status launch_kv4_attention(const Kv4Cache &c, const void *q, int64_t q_stride, int64_t q_heads,

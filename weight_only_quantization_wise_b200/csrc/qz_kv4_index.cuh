@@ -81,16 +81,33 @@ QZ_HD int64_t record_index(const int32_t *row, int64_t max_pages, int64_t num_pa
     return ((int64_t)page * kv_heads + h) * page_blocks + (block - pi * page_blocks);
 }
 
-// Sequence that owns token t: the b with cu[b] <= t < cu[b + 1]; -1 when no
-// sequence does (tokens behind the last one).
-QZ_HD int64_t find_sequence(const int32_t *cu, int64_t B, int64_t t) {
-    int64_t lo = 0, hi = B;                   // first b with cu[b + 1] > t
-    while (lo < hi) {
-        const int64_t mid = (lo + hi) >> 1;
-        if ((int64_t)cu[mid + 1] > t) hi = mid;
-        else lo = mid + 1;
-    }
-    return lo < B && (int64_t)cu[lo] <= t ? lo : -1;
+// ---- append's and read's work --------------------------------------------
+// A sequence's n tokens (rows cu0 .. cu0 + n - 1) stand at positions first ..
+// first + n - 1, first = kv_len - n (negative when the length is too small).
+// A unit is (block of 16 positions, head), heads fastest; block i of the
+// sequence holds positions 16 (block0 + i) ...
+struct StoreWork {
+    int n, block0, blocks;
+    int64_t first, units;
+};
+QZ_HD StoreWork store_work(int cu0, int cu1, int kv_len, int rows, int kv_heads) {
+    StoreWork s;
+    s.n = cu0 >= 0 && cu1 > cu0 ? cu1 - cu0 : 0;
+    if (s.n > rows) s.n = rows;
+    s.first = (int64_t)kv_len - s.n;
+    s.block0 = (int)(s.first >> 4);                // rounds down
+    s.blocks = s.n > 0 ? (int)(((int64_t)kv_len - 1) >> 4) - s.block0 + 1 : 0;
+    s.units = (int64_t)s.blocks * kv_heads;
+    return s;
+}
+// Tokens [lo, hi) of block `block` that are the sequence's.
+QZ_HD int block_lo(const StoreWork &s, int block) {
+    const int64_t d = s.first - (int64_t)block * kBlock;
+    return d > 0 ? (int)d : 0;
+}
+QZ_HD int block_hi(const StoreWork &s, int block) {
+    const int64_t d = s.first + s.n - (int64_t)block * kBlock;
+    return d < kBlock ? (int)d : kBlock;
 }
 
 // ---- attention's work ---------------------------------------------------
