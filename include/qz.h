@@ -88,7 +88,9 @@ enum {
     QZ_OP_GPTQ = 6,
     QZ_OP_FP4A16_GEMV = 7,
     QZ_OP_FP4A4_GEMM = 8,
-    QZ_OP_KV4_ATTENTION = 9     /* K = head_dim; M, N (>= 1) and group_size are not used */
+    QZ_OP_KV4_ATTENTION = 9,    /* K = head_dim; M, N (>= 1) and group_size are not used */
+    QZ_OP_W4A16_LORA_GEMV = 10,
+    QZ_OP_W8A16_LORA_GEMV = 11
 };
 
 /* FP4 formats (kind argument of the qz_fp4_* entry points). */
@@ -366,6 +368,37 @@ QZ_API qz_status qz_fp4a4_gemm(const void *a, const void *codes, const void *sca
                                const void *tensor_scale, int64_t M, int64_t N, int64_t K,
                                int32_t kind, void *y, void *workspace, size_t workspace_bytes,
                                void *stream);
+
+/*
+ * Decode GEMV with a low-rank adapter per token: the projections of
+ * qz_w4a16_gemv and qz_w8a16_gemv (same formats, same 1 <= M <= 64) with
+ *   y_m = a_m * w_hat^T + lora_scales[r] * (a_m * A_r^T) * B_r^T,  r = adapters[m],
+ * summed in fp32 and rounded once to bf16; a token with a negative adapter
+ * gets the projection alone.  The low-rank product a_m * A_r^T is held to
+ * 2^-17.
+ *   lora_a      bf16 [n_adapters][rank][K], 16-byte aligned
+ *   lora_b      bf16 [n_adapters][N][rank], 16-byte aligned
+ *   adapters    int32 [M], read on the device: an index >= n_adapters counts as
+ *               none, and the next qz_device_status reports QZ_ERR_DEVICE_INDEX
+ *   lora_scales fp32 [n_adapters]
+ * rank: a multiple of 8, at most 128 (adapters of lower rank are padded with
+ * zeros).  Only adapters in use are read, each once.  Other arguments,
+ * requirements and errors as for the plain GEMVs.  Workspace:
+ * qz_workspace_bytes(QZ_OP_W4A16_LORA_GEMV, M, N, K, group_size) or
+ * (QZ_OP_W8A16_LORA_GEMV, M, N, K, K) bytes, zero-filled before first use.
+ */
+QZ_API qz_status qz_w4a16_lora_gemv(const void *a, const void *codes, const void *scales,
+                                    const void *zeros, int64_t M, int64_t N, int64_t K,
+                                    int64_t group_size, const void *lora_a, const void *lora_b,
+                                    const void *adapters, const void *lora_scales,
+                                    int64_t n_adapters, int64_t rank, void *y, void *workspace,
+                                    size_t workspace_bytes, void *stream);
+QZ_API qz_status qz_w8a16_lora_gemv(const void *a, const void *codes, const void *scales,
+                                    int64_t M, int64_t N, int64_t K, const void *lora_a,
+                                    const void *lora_b, const void *adapters,
+                                    const void *lora_scales, int64_t n_adapters, int64_t rank,
+                                    void *y, void *workspace, size_t workspace_bytes,
+                                    void *stream);
 
 /*
  * Paged 4-bit key/value cache.

@@ -75,12 +75,13 @@ def attention(q, kv, lens, new, scale, window, masked=None):
 
     q: (T, Hq, D) float64; kv: list of (k^, v^, S_v max per key) per sequence,
     each (len, H, D) float64.  masked[b]: keys to leave out.  Returns out, and
-    per output the bound's parts: sum P|v|, sum P S, max P S, |scale| max|q| sum|k|.
+    per output the bound's parts: sum P|v|, sum P S, max P S, |scale| max|q| sum|k|,
+    the keys seen, max|v|.
     """
     T, Hq, D = q.shape
     out = np.zeros((T, Hq, D))
     parts = dict(pv=np.zeros((T, Hq, D)), ps=np.zeros((T, Hq, 1)), mps=np.zeros((T, Hq, 1)),
-                 dq=np.zeros((T, Hq, 1)), keys=np.zeros((T, Hq, 1)))
+                 dq=np.zeros((T, Hq, 1)), keys=np.zeros((T, Hq, 1)), mv=np.zeros((T, Hq, D)))
     row = 0
     for b, (L, n) in enumerate(zip(lens, new)):
         for i in range(n):
@@ -107,6 +108,7 @@ def attention(q, kv, lens, new, scale, window, masked=None):
                     parts["mps"][row, h] = (P * S).max()
                     parts["dq"][row, h] = abs(scale) * np.abs(qh).max() * np.abs(kh).sum(-1).max()
                     parts["keys"][row, h] = keep.sum()
+                    parts["mv"][row, h] = np.abs(vh).max(0)
             row += 1
     return out, parts
 
@@ -121,13 +123,16 @@ def bound(out, parts, D):
     to its largest value, at most 2^-15 of that off, so a score moves by at most
     |scale| 2^-15 max|q| sum|k|; its integer sum is exact, and the conversion
     and two products round it by less than 2^-21 of |scale| max|q| sum|k|.
-    That moves each P by a factor of at most e^(2 delta); ex2 and the fp32 sums
-    add 2^-20.  The sum over keys: the tensor core adds 16 products and the
+    That moves each P by a factor of at most e^(2 delta), and sum |P' - P| |v| by
+    no more than 2 max|v| however large delta is (both P sum to 1); ex2 and the
+    fp32 sums add 2^-20.  The sum over keys: the tensor core adds 16 products and the
     accumulator with an error of at most 2^-22 of the largest magnitude, sum P S
     15, each time.
     """
     delta = parts["dq"] * (2.0 ** -15 + 2.0 ** -21)
     return (2.0 ** -8 * np.abs(out) +
-            (2.0 ** -11 + 2.0 ** -20 + np.expm1(2 * delta)) * parts["pv"] * (1 + 2.0 ** -8) +
+            ((2.0 ** -11 + 2.0 ** -20) * parts["pv"] +
+             np.minimum(np.expm1(np.minimum(2 * delta, 60)) * parts["pv"], 2 * parts["mv"])) *
+            (1 + 2.0 ** -8) +
             (parts["keys"] / 16 + 8) * 2.0 ** -22 * 15 * parts["ps"] +
             parts["keys"] * 15 * 2.0 ** -24 * parts["mps"] + 2.0 ** -133)

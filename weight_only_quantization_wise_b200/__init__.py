@@ -24,7 +24,8 @@ __all__ = [
     "QZ_OP_FP4A16_GEMV", "QZ_FP4_MX", "QZ_FP4_NV", "qz_fp4_mma_scale_bytes",
     "qz_fp4_scales_to_mma", "qz_fp4a4_gemm", "QZ_OP_FP4A4_GEMM",
     "qz_kv4_cache_bytes", "qz_kv4_append", "qz_kv4_read", "qz_kv4_attention",
-    "QZ_OP_KV4_ATTENTION",
+    "QZ_OP_KV4_ATTENTION", "qz_w4a16_lora_gemv", "qz_w8a16_lora_gemv", "QZ_OP_W4A16_LORA_GEMV",
+    "QZ_OP_W8A16_LORA_GEMV",
     "Workspace", "QZ_OP_QUANTIZE_PACK", "QZ_OP_DEQUANTIZE", "QZ_OP_W4A16_GEMV",
     "QZ_OP_W4A16_GEMM", "QZ_OP_W8A16_GEMV", "QZ_OP_W8A16_GEMM", "EXPORTED_SYMBOLS",
 ]
@@ -36,7 +37,7 @@ QZ_ERR_DEVICE_TIMEOUT = 6
 QZ_ERR_DEVICE_INDEX = 7
 (QZ_OP_QUANTIZE_PACK, QZ_OP_DEQUANTIZE, QZ_OP_W4A16_GEMV, QZ_OP_W4A16_GEMM, QZ_OP_W8A16_GEMV,
  QZ_OP_W8A16_GEMM, QZ_OP_GPTQ, QZ_OP_FP4A16_GEMV, QZ_OP_FP4A4_GEMM,
- QZ_OP_KV4_ATTENTION) = range(10)
+ QZ_OP_KV4_ATTENTION, QZ_OP_W4A16_LORA_GEMV, QZ_OP_W8A16_LORA_GEMV) = range(12)
 QZ_FP4_MX, QZ_FP4_NV = 0, 1
 FP4_BLOCK = {QZ_FP4_MX: 32, QZ_FP4_NV: 16}
 
@@ -67,6 +68,10 @@ _SIGS = {
     "qz_fp4_mma_scale_bytes": ([_i64, _i64, _i32, ctypes.POINTER(_sz)], ctypes.c_int),
     "qz_fp4_scales_to_mma": ([_p, _i64, _i64, _i32, _p, _p], ctypes.c_int),
     "qz_fp4a4_gemm": ([_p, _p, _p, _p, _i64, _i64, _i64, _i32, _p, _p, _sz, _p], ctypes.c_int),
+    "qz_w4a16_lora_gemv": ([_p] * 4 + [_i64] * 4 + [_p] * 4 + [_i64] * 2 + [_p, _p, _sz, _p],
+                           ctypes.c_int),
+    "qz_w8a16_lora_gemv": ([_p] * 3 + [_i64] * 3 + [_p] * 4 + [_i64] * 2 + [_p, _p, _sz, _p],
+                           ctypes.c_int),
     "qz_kv4_cache_bytes": ([_i64, _i64, _i64, _i64, _i64, ctypes.POINTER(_sz)], ctypes.c_int),
     "qz_kv4_append": ([_p, _p, _p, _i64, _i64, _p, _p, _p] + [_i64] * 8 + [_p], ctypes.c_int),
     "qz_kv4_read": ([_p, _p, _p, _p] + [_i64] * 8 + [_p, _p, _p], ctypes.c_int),
@@ -461,6 +466,77 @@ def qz_fp4a4_gemm(a, codes, scales_mma, tensor_scale, N, K, kind, y=None, worksp
 
 
 # ---------------------------------------------------------------------------
+# low-rank adapters beside a packed projection
+# ---------------------------------------------------------------------------
+def _lora_args(a, N, K, lora_a, lora_b, adapters, lora_scales):
+    """Addresses of the adapter arrays, adapters and rank."""
+    dev = a.device
+    if a.dtype is not torch.bfloat16 or a.dim() != 2 or a.shape[1] != K or not a.is_cuda:
+        raise ValueError("a must be an (M, K) bf16 tensor on a CUDA device")
+    if (lora_a.dtype is not torch.bfloat16 or lora_b.dtype is not torch.bfloat16 or
+            lora_a.dim() != 3 or lora_b.dim() != 3):
+        raise ValueError("lora_a and lora_b must be 3-D bf16 tensors")
+    n, rank = lora_a.shape[0], lora_a.shape[1]
+    if lora_a.shape[2] != K or lora_b.shape[0] != n or lora_b.shape[1] != N or \
+            lora_b.shape[2] != rank:
+        raise ValueError("lora_a must be (adapters, rank, K) and lora_b (adapters, N, rank)")
+    if adapters.dtype is not torch.int32 or adapters.dim() != 1 or \
+            adapters.shape[0] != a.shape[0]:
+        raise ValueError("adapters must be an int32 tensor of M indices")
+    if lora_scales.dtype is not torch.float32 or lora_scales.dim() != 1 or \
+            lora_scales.shape[0] != n:
+        raise ValueError("lora_scales must be an fp32 tensor with one value per adapter")
+    for t in (a, lora_a, lora_b, adapters, lora_scales):
+        if t.device != dev or not t.is_contiguous():
+            raise ValueError("a and the adapter tensors must be contiguous and on one device")
+    return (lora_a.data_ptr(), lora_b.data_ptr(), adapters.data_ptr(), lora_scales.data_ptr(), n,
+            rank)
+
+
+def _lora_out(a, N, y):
+    if y is None:
+        return torch.empty((a.shape[0], N), dtype=torch.bfloat16, device=a.device)
+    if y.dtype is not torch.bfloat16 or tuple(y.shape) != (a.shape[0], N) or y.device != a.device:
+        raise ValueError("y must be an (M, N) bf16 tensor on a's device")
+    return y
+
+
+def qz_w4a16_lora_gemv(a, codes, scales, zeros, N, K, lora_a, lora_b, adapters, lora_scales,
+                       group_size=128, y=None, workspace=None, stream=None):
+    """y = a * w_hat^T + lora_scales[r] * (a * A_r^T) * B_r^T for int4 asymmetric
+    weights, M <= 64 tokens, each with the adapter r = adapters[m] (none when
+    negative).  lora_a: (adapters, rank, K), lora_b: (adapters, N, rank) bf16."""
+    dev = a.device
+    la, lb, ids, ls, n, rank = _lora_args(a, N, K, lora_a, lora_b, adapters, lora_scales)
+    M = a.shape[0]
+    with _scope(dev, stream):
+        y = _lora_out(a, N, y)
+        nbytes = qz_workspace_bytes(QZ_OP_W4A16_LORA_GEMV, M, N, K, group_size)
+        ws_ptr, ws_bytes = _ws_args(workspace, nbytes, dev, _matmul_key(
+            QZ_OP_W4A16_LORA_GEMV, M, N, K, group_size, scales, zeros))
+        _check(lib.qz_w4a16_lora_gemv(a.data_ptr(), _ptr(codes), _ptr(scales), _ptr(zeros), M, N, K,
+                                      group_size, la, lb, ids, ls, n, rank, _ptr(y), ws_ptr,
+                                      ws_bytes, _stream_of(dev, stream)), "qz_w4a16_lora_gemv")
+    return y
+
+
+def qz_w8a16_lora_gemv(a, codes, scales, N, K, lora_a, lora_b, adapters, lora_scales, y=None,
+                       workspace=None, stream=None):
+    """The same for int8 symmetric per-channel weights."""
+    dev = a.device
+    la, lb, ids, ls, n, rank = _lora_args(a, N, K, lora_a, lora_b, adapters, lora_scales)
+    M = a.shape[0]
+    with _scope(dev, stream):
+        y = _lora_out(a, N, y)
+        nbytes = qz_workspace_bytes(QZ_OP_W8A16_LORA_GEMV, M, N, K, K)
+        ws_ptr, ws_bytes = _ws_args(workspace, nbytes, dev, (QZ_OP_W8A16_LORA_GEMV, M, N, K))
+        _check(lib.qz_w8a16_lora_gemv(a.data_ptr(), _ptr(codes), _ptr(scales), M, N, K, la, lb, ids,
+                                      ls, n, rank, _ptr(y), ws_ptr, ws_bytes,
+                                      _stream_of(dev, stream)), "qz_w8a16_lora_gemv")
+    return y
+
+
+# ---------------------------------------------------------------------------
 # paged 4-bit key/value cache
 # ---------------------------------------------------------------------------
 _KV4_BYTES = {}
@@ -503,9 +579,16 @@ def _scope(dev, stream):
     return _Scope(dev, stream)
 
 
+# the current stream's handle without a Stream object (3 us less per call)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _stream_of(dev, stream):
     """Handle of the stream a call runs on: `stream`, else `dev`'s current one."""
-    return (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
+    if stream is None:
+        return _current_raw_stream(torch.cuda.current_device() if dev.index is None else dev.index)
+    return stream.cuda_stream
 
 
 def _heads(t, name, dev):

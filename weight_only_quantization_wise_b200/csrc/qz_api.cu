@@ -95,6 +95,14 @@ qz_status check_fp4a4(int64_t M, int64_t N, int64_t K, int32_t kind) {
     return QZ_OK;
 }
 
+// The GEMV's part of a LoRA GEMV's workspace (a multiple of 256 bytes; the
+// adapters' scratch lies behind it).
+size_t lora_gemv_bytes(int bits, int64_t M, int64_t N, int64_t K, int64_t group_size) {
+    const size_t b = bits == 4 ? gemv_workspace_bound(M, N, K, 4, gemv_unit_k(4, M, N, K, group_size))
+                               : gemv_workspace_bound(M, N, K, 8);
+    return (b + 255) & ~(size_t)255;
+}
+
 }  // namespace
 }  // namespace qz
 
@@ -178,6 +186,14 @@ QZ_API qz_status qz_workspace_bytes(int32_t op, int64_t M, int64_t N, int64_t K,
         const qz_status s = check_fp4a4(M, N, K, QZ_FP4_NV);
         if (s != QZ_OK) return s;
         *bytes = fp4a4_workspace_bytes(M, K);
+        return QZ_OK;
+    }
+    case QZ_OP_W4A16_LORA_GEMV:
+    case QZ_OP_W8A16_LORA_GEMV: {
+        const qz_status s = check_gemv_shape(M, N, K);
+        if (s != QZ_OK) return s;
+        *bytes = lora_gemv_bytes(op == QZ_OP_W4A16_LORA_GEMV ? 4 : 8, M, N, K, group_size) +
+                 lora_scratch_bytes(M, N);
         return QZ_OK;
     }
     case QZ_OP_KV4_ATTENTION:
@@ -454,6 +470,75 @@ QZ_API qz_status qz_fp4a4_gemm(const void *a, const void *codes, const void *sca
     if (s != QZ_OK) return s;
     return launch_fp4a4_gemm(a, codes, scales_mma, tensor_scale, M, N, K, kind, y, workspace,
                              as_stream(stream));
+}
+
+namespace {
+
+// Shared by both formats: the base projection's arguments have been checked.
+qz_status lora_gemv(int bits, const void *a, const void *codes, const void *scales,
+                    const void *zeros, int64_t M, int64_t N, int64_t K, int64_t group_size,
+                    const void *lora_a, const void *lora_b, const void *adapters,
+                    const void *lora_scales, int64_t n_adapters, int64_t rank, void *y,
+                    void *workspace, size_t workspace_bytes, cudaStream_t st) {
+    if (n_adapters < 1 || rank < 1 || n_adapters > kMaxDim) return QZ_ERR_INVALID_ARG;
+    if (rank % 8 != 0 || rank > kLoraMaxRank) return QZ_ERR_UNSUPPORTED;
+    if (n_adapters > kMaxElems / (rank * (N > K ? N : K))) return QZ_ERR_INVALID_ARG;
+    if (!lora_a || !lora_b || !adapters || !lora_scales) return QZ_ERR_INVALID_ARG;
+    if (!aligned(lora_a, 16) || !aligned(lora_b, 16) || !aligned(adapters, 4) ||
+        !aligned(lora_scales, 4))
+        return QZ_ERR_ALIGNMENT;
+    const size_t base = lora_gemv_bytes(bits, M, N, K, group_size);
+    qz_status s = check_workspace(base + lora_scratch_bytes(M, N), workspace, workspace_bytes);
+    if (s != QZ_OK) return s;
+    const GemvPlan plan =
+        bits == 4 ? gemv_plan(M, N, K, 4, device_sm_count(),
+                              gemv_unit_k(4, M, N, K, group_size, scales, zeros))
+                  : gemv_plan(M, N, K, 8, device_sm_count());
+    const float *delta = nullptr;
+    s = launch_lora(a, lora_a, lora_b, adapters, lora_scales, n_adapters, rank, M, N, K,
+                    static_cast<char *>(workspace) + base, &delta, st);
+    if (s != QZ_OK) return s;
+    // The GEMV always overlaps the adapters' kernels (mode 1 of
+    // qz_set_launch_overlap): they do not write the weights, and the first of
+    // them starts only after whatever was queued before this call.
+    return launch_gemv_add(bits, a, codes, scales, zeros, M, N, K, group_size, delta, y, workspace,
+                           plan, 1, st);
+}
+
+}  // namespace
+
+QZ_API qz_status qz_w4a16_lora_gemv(const void *a, const void *codes, const void *scales,
+                                    const void *zeros, int64_t M, int64_t N, int64_t K,
+                                    int64_t group_size, const void *lora_a, const void *lora_b,
+                                    const void *adapters, const void *lora_scales,
+                                    int64_t n_adapters, int64_t rank, void *y, void *workspace,
+                                    size_t workspace_bytes, void *stream) {
+    const qz_status s = check_gemv_shape(M, N, K);
+    if (s != QZ_OK) return s;
+    if (group_size < 32 || group_size % 32 != 0 || K % group_size != 0)
+        return group_size <= 0 || K % group_size != 0 ? QZ_ERR_INVALID_ARG : QZ_ERR_UNSUPPORTED;
+    if (!a || !codes || !scales || !zeros || !y) return QZ_ERR_INVALID_ARG;
+    if (!aligned(a, 16) || !aligned(codes, 16) || !aligned(scales, 2) || !aligned(y, 2))
+        return QZ_ERR_ALIGNMENT;
+    return lora_gemv(4, a, codes, scales, zeros, M, N, K, group_size, lora_a, lora_b, adapters,
+                     lora_scales, n_adapters, rank, y, workspace, workspace_bytes,
+                     as_stream(stream));
+}
+
+QZ_API qz_status qz_w8a16_lora_gemv(const void *a, const void *codes, const void *scales,
+                                    int64_t M, int64_t N, int64_t K, const void *lora_a,
+                                    const void *lora_b, const void *adapters,
+                                    const void *lora_scales, int64_t n_adapters, int64_t rank,
+                                    void *y, void *workspace, size_t workspace_bytes,
+                                    void *stream) {
+    const qz_status s = check_gemv_shape(M, N, K);
+    if (s != QZ_OK) return s;
+    if (!a || !codes || !scales || !y) return QZ_ERR_INVALID_ARG;
+    if (!aligned(a, 16) || !aligned(codes, 16) || !aligned(scales, 2) || !aligned(y, 2))
+        return QZ_ERR_ALIGNMENT;
+    return lora_gemv(8, a, codes, scales, nullptr, M, N, K, K, lora_a, lora_b, adapters,
+                     lora_scales, n_adapters, rank, y, workspace, workspace_bytes,
+                     as_stream(stream));
 }
 
 namespace {

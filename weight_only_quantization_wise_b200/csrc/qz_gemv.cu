@@ -305,6 +305,7 @@ struct GemvArgs {
     int bpg_shift;             // log2(group_size / 128) (ring path), else -1
     int kblocks;               // K / 128
     uint16_t *y;
+    const float *addend;       // M x N fp32 added to the sums before the rounding (ADD variants)
     float *partials;
     uint32_t *counters;
     int64_t units;             // tasks * kblocks
@@ -612,7 +613,9 @@ __device__ __forceinline__ void gemv_flush(float (&acc)[2][MB][4], const GemvArg
 // 128-byte row of codes per weight row, consumed as two halves).  ACTSW
 // (two-half units): activations as four swizzled 64-k boxes (load_act_sw),
 // else one box of 256 k (one token: its lanes of equal t read the same words).
-template <int BITS, int MB, int META, int FMT, int HALVES = 1, bool ACTSW = true>
+// ADD: the sums of a task start from p.addend, in the CTA that covers the
+// task's first K block.
+template <int BITS, int MB, int META, int FMT, int HALVES = 1, bool ACTSW = true, bool ADD = false>
 __global__ void __launch_bounds__(kThreads, (kCtasPerSm<MB, HALVES>))
 gemv_kernel(const __grid_constant__ CUtensorMap code_map,
             const __grid_constant__ CUtensorMap act_map,
@@ -833,6 +836,21 @@ gemv_kernel(const __grid_constant__ CUtensorMap code_map,
                 for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) acc[c][rt][mb][j] = 0.0f;
+        if constexpr (ADD) {
+            if (kb0 == 0) {
+#pragma unroll
+                for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+                    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int row = n0 + 16 * rt + g + 8 * (j >> 1);
+                            const int tok = 8 * mb + 2 * t + (j & 1);
+                            if (row < p.N && tok < p.M)
+                                acc[0][rt][mb][j] = __ldcg(p.addend + (int64_t)tok * p.N + row);
+                        }
+            }
+        }
 
         for (int kb = kb0; kb < kb_end; ++kb) {
             int m = 0;
@@ -1055,7 +1073,7 @@ struct Maps {
     CUtensorMap code, act, scale, zero;
 };
 
-template <int BITS, int MB, int META, int FMT, int HALVES = 1, bool ACTSW = true>
+template <int BITS, int MB, int META, int FMT, int HALVES = 1, bool ACTSW = true, bool ADD = false>
 qz_status launch_variant(const Maps &maps, const GemvArgs &args, dim3 grid, int overlap,
                          cudaStream_t st) {
     constexpr int smem = Layout<BITS, MB, META, FMT, HALVES>::bytes;
@@ -1066,13 +1084,13 @@ qz_status launch_variant(const Maps &maps, const GemvArgs &args, dim3 grid, int 
         return QZ_ERR_CUDA;
     }
     if (attr_once.run(dev, [] {
-            cudaError_t e = cudaFuncSetAttribute(gemv_kernel<BITS, MB, META, FMT, HALVES, ACTSW>,
+            cudaError_t e = cudaFuncSetAttribute(gemv_kernel<BITS, MB, META, FMT, HALVES, ACTSW, ADD>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  smem);
             // three rings per SM need (nearly) all of the unified memory as
             // shared memory
             if (e == cudaSuccess)
-                e = cudaFuncSetAttribute(gemv_kernel<BITS, MB, META, FMT, HALVES, ACTSW>,
+                e = cudaFuncSetAttribute(gemv_kernel<BITS, MB, META, FMT, HALVES, ACTSW, ADD>,
                                          cudaFuncAttributePreferredSharedMemoryCarveout, 100);
             return e;
         }) != cudaSuccess)
@@ -1087,19 +1105,21 @@ qz_status launch_variant(const Maps &maps, const GemvArgs &args, dim3 grid, int 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = overlap > 0 ? 1 : 0;
-    cudaLaunchKernelEx(&cfg, gemv_kernel<BITS, MB, META, FMT, HALVES, ACTSW>, maps.code, maps.act,
+    cudaLaunchKernelEx(&cfg, gemv_kernel<BITS, MB, META, FMT, HALVES, ACTSW, ADD>, maps.code, maps.act,
                        maps.scale, maps.zero, args);
     return launch_status();
 }
 
-template <int BITS, int META, int FMT = kFmtInt>
+template <int BITS, int META, int FMT = kFmtInt, bool ADD = false>
 qz_status launch_mb(const Maps &maps, const GemvArgs &args, dim3 grid, int overlap,
                     cudaStream_t st) {
-    if (args.M <= 8) return launch_variant<BITS, 1, META, FMT>(maps, args, grid, overlap, st);
+    if (args.M <= 8)
+        return launch_variant<BITS, 1, META, FMT, 1, true, ADD>(maps, args, grid, overlap, st);
     if (args.M <= 16 || FMT != kFmtInt)
-        return launch_variant<BITS, 2, META, FMT>(maps, args, grid, overlap, st);
-    if (args.M <= 32) return launch_variant<BITS, 4, META, kFmtInt>(maps, args, grid, overlap, st);
-    return launch_variant<BITS, 8, META, kFmtInt>(maps, args, grid, overlap, st);
+        return launch_variant<BITS, 2, META, FMT, 1, true, ADD>(maps, args, grid, overlap, st);
+    if (args.M <= 32)
+        return launch_variant<BITS, 4, META, kFmtInt, 1, true, ADD>(maps, args, grid, overlap, st);
+    return launch_variant<BITS, 8, META, kFmtInt, 1, true, ADD>(maps, args, grid, overlap, st);
 }
 
 // How the int4 GEMV's scales and zeros reach shared memory: as TMA tiles
@@ -1127,10 +1147,11 @@ bool two_half_ok(int64_t M, int64_t N, int64_t K, int64_t group_size, const void
     return meta == kMetaGather && (group_size > kBlockK || (K / group_size) % 2 == 0);
 }
 
-template <int BITS>
+template <int BITS, bool ADD = false>
 qz_status launch_gemv(const void *a, const void *codes, const void *scales, const void *zeros,
                       int64_t M, int64_t N, int64_t K, int64_t group_size, void *y,
-                      void *workspace, const GemvPlan &plan, int overlap, cudaStream_t st) {
+                      void *workspace, const GemvPlan &plan, int overlap, cudaStream_t st,
+                      const float *addend = nullptr) {
     GemvArgs args;
     args.scales = static_cast<const uint16_t *>(scales);
     args.fp4_scales = nullptr;
@@ -1147,6 +1168,7 @@ qz_status launch_gemv(const void *a, const void *codes, const void *scales, cons
     args.meta_span_shift = args.bpg_shift >= 0 ? args.bpg_shift + 3 - (halves - 1) : 0;
     args.kblocks = (int)(K / plan.unit_k);
     args.y = static_cast<uint16_t *>(y);
+    args.addend = addend;
     args.partials = nullptr;
     args.counters = nullptr;
     if (plan.total_bytes > 0) {
@@ -1194,29 +1216,29 @@ qz_status launch_gemv(const void *a, const void *codes, const void *scales, cons
                                     CU_TENSOR_MAP_SWIZZLE_NONE))
                 return QZ_ERR_CUDA;
             if (halves == 2)
-                return M == 1   ? launch_variant<4, 1, kMetaTma, kFmtInt, 2, false>(maps, args, grid,
+                return M == 1   ? launch_variant<4, 1, kMetaTma, kFmtInt, 2, false, ADD>(maps, args, grid,
                                                                                    overlap, st)
-                       : M <= 8 ? launch_variant<4, 1, kMetaTma, kFmtInt, 2>(maps, args, grid,
+                       : M <= 8 ? launch_variant<4, 1, kMetaTma, kFmtInt, 2, true, ADD>(maps, args, grid,
                                                                           overlap, st)
-                              : launch_variant<4, 2, kMetaTma, kFmtInt, 2>(maps, args, grid,
+                              : launch_variant<4, 2, kMetaTma, kFmtInt, 2, true, ADD>(maps, args, grid,
                                                                           overlap, st);
-            return launch_mb<4, kMetaTma>(maps, args, grid, overlap, st);
+            return launch_mb<4, kMetaTma, kFmtInt, ADD>(maps, args, grid, overlap, st);
         }
         // The gather path copies the aligned 4-byte words holding each scale
         // and zero.
         if (meta == kMetaGather) {
             if (halves == 2)
-                return M == 1   ? launch_variant<4, 1, kMetaGather, kFmtInt, 2, false>(maps, args, grid,
+                return M == 1   ? launch_variant<4, 1, kMetaGather, kFmtInt, 2, false, ADD>(maps, args, grid,
                                                                                    overlap, st)
-                       : M <= 8 ? launch_variant<4, 1, kMetaGather, kFmtInt, 2>(maps, args, grid,
+                       : M <= 8 ? launch_variant<4, 1, kMetaGather, kFmtInt, 2, true, ADD>(maps, args, grid,
                                                                           overlap, st)
-                              : launch_variant<4, 2, kMetaGather, kFmtInt, 2>(maps, args, grid,
+                              : launch_variant<4, 2, kMetaGather, kFmtInt, 2, true, ADD>(maps, args, grid,
                                                                              overlap, st);
-            return launch_mb<4, kMetaGather>(maps, args, grid, overlap, st);
+            return launch_mb<4, kMetaGather, kFmtInt, ADD>(maps, args, grid, overlap, st);
         }
-        return launch_mb<4, kMetaNone>(maps, args, grid, overlap, st);
+        return launch_mb<4, kMetaNone, kFmtInt, ADD>(maps, args, grid, overlap, st);
     } else {
-        return launch_mb<8, kMetaNone>(maps, args, grid, overlap, st);
+        return launch_mb<8, kMetaNone, kFmtInt, ADD>(maps, args, grid, overlap, st);
     }
 }
 
@@ -1382,6 +1404,17 @@ qz_status launch_w8a16_gemv(const void *a, const void *codes, const void *scales
                             const GemvPlan &plan, int overlap, cudaStream_t st) {
     return launch_gemv<8>(a, codes, scales, nullptr, M, N, K, K, y, workspace, plan, overlap,
                           st);
+}
+
+qz_status launch_gemv_add(int bits, const void *a, const void *codes, const void *scales,
+                          const void *zeros, int64_t M, int64_t N, int64_t K, int64_t group_size,
+                          const float *addend, void *y, void *workspace, const GemvPlan &plan,
+                          int overlap, cudaStream_t st) {
+    if (bits == 4)
+        return launch_gemv<4, true>(a, codes, scales, zeros, M, N, K, group_size, y, workspace,
+                                    plan, overlap, st, addend);
+    return launch_gemv<8, true>(a, codes, scales, nullptr, M, N, K, K, y, workspace, plan, overlap,
+                                st, addend);
 }
 
 }  // namespace qz

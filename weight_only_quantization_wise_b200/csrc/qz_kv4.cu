@@ -515,12 +515,11 @@ __global__ void __launch_bounds__(kStoreThreads) kv4_read_kernel(const StoreArgs
 // tensor core aligns a subnormal's products by its nominal exponent and loses
 // their low bits: 2^-15 of the largest product, seen where one key holds the
 // weight and c = Z.)
-// The weights w_j = P_j S_j are rounded once to fp16 (2^-11 of each) for the
-// second product.  One running maximum n per row, of s_j + log2 S_j (all in
-// powers of two), scales both sums: w_j = 2^(s_j - n) S_j lies below 2^4
-// whatever the sizes of V, and the softmax's sum l of 2^(s_j - n) is fp32; the
-// result is the quotient of the two sums.  log2 S_j is kept within -+100, so
-// that l neither overflows nor vanishes.
+// The weights P_j S_j are rounded once to fp16 (2^-11 of each) for the second
+// product: w_j = 2^(s_j - m) S_j 2^-E, m a row's running maximum of s_j (in
+// powers of two) and E one exponent per warp that keeps the largest weight
+// near 1 whatever the sizes of V.  Both move only when a weight reaches 2^12
+// (fp16 holds those below 2^16).  The softmax's sum l of 2^(s_j - m) is fp32.
 //
 // Work.  Warps work alone: a warp takes a contiguous range of (head, block)
 // units, keeps records of 16 tokens in a ring of its own (two per stage, one
@@ -547,13 +546,14 @@ struct AttnArgs {
 };
 
 constexpr float kNoMax = -1e30f;       // running maximum before any key
+constexpr int kNoExp = -1000;          // E before any key
 
-// A partial result of a row tile: [R][D + 4] fp32 sums, then n and l per row.
+// A partial result of a row tile: [R][D + 4] fp32 sums, then m and l per row.
 template <int D, int NB>
 struct Slot {
     static constexpr int R = 8 * NB;
     static constexpr int pitch = D + 4;                    // floats: rows 8 apart in banks
-    static constexpr int stats = R * pitch;                // n[R], l[R]
+    static constexpr int stats = R * pitch;                // m[R], l[R]
     static constexpr int floats = R * pitch + 2 * R;
     static constexpr int bytes = floats * 4;
 };
@@ -594,11 +594,6 @@ struct Part {                          // a warp's part of an item
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ float lg2(float x) {
-    float r;
-    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -942,7 +937,8 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                 }
 
             // ---- main loop ----
-            float acc[4 * VW][NB][4], l[NB][2], nm[NB][2];
+            float acc[4 * VW][NB][4], l[NB][2], m[NB][2], vf = 1.0f;
+            int ve = kNoExp;                       // E; vf = 2^-E
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -952,7 +948,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     l[nb][c] = 0.0f;
-                    nm[nb][c] = kNoMax;
+                    m[nb][c] = kNoMax;
                 }
             }
             for (int i = 0; i < steps; ++i) {
@@ -972,7 +968,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                     const uint8_t *st0 = smem + L::ring_off + warp * L::ring + 2 * stage * L::rec;
                     const uint8_t *sr[2] = {got == 2u ? st0 + L::rec : st0,
                                             got == 1u ? st0 : st0 + L::rec};
-                    float s[2][NB][4], vs[2][NG][2], vl[2][2];
+                    float s[2][NB][4], vs[2][NG][2];
                     // -- scores (without kq): tokens gid and gid + 8 of each
                     //    record, columns 2 tig, 2 tig + 1
                     uint32_t kw[2][2][KW];
@@ -1039,20 +1035,15 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                                     }
                             }
                     }
-                    // -- V scales, log2 of the largest
+                    // -- V scales
 #pragma unroll
                     for (int rc = 0; rc < 2; ++rc)
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            float top = 0.0f;
+                        for (int x = 0; x < 2; ++x)
 #pragma unroll
-                            for (int gr = 0; gr < NG; ++gr) {
+                            for (int gr = 0; gr < NG; ++gr)
                                 vs[rc][gr][x] =
                                     bf16_at(sr[rc] + v_scales_off(D, NG) + 32 * gr + 2 * (gid + 8 * x));
-                                top = fmaxf(top, vs[rc][gr][x]);
-                            }
-                            vl[rc][x] = fminf(fmaxf(lg2(top), -100.0f), 100.0f);
-                        }
                     // -- scores in powers of two, masks
 #pragma unroll
                     for (int rc = 0; rc < 2; ++rc)
@@ -1072,7 +1063,6 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                                 const int key = key0 + 16 * rc + gid + 8 * x;
                                 const bool none = !((got >> rc) & 1u) || key >= sw.len;
                                 if (none) {                     // not written: whatever it holds
-                                    vl[rc][x] = 0.0f;
 #pragma unroll
                                     for (int gr = 0; gr < NG; ++gr) vs[rc][gr][x] = 0.0f;
                                 }
@@ -1084,46 +1074,80 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                                             s[rc][nb][2 * x + c] = __int_as_float(0xFF800000);
                             }
                     }
-                    // -- s minus the running maximum; the maximum is raised only when
-                    //    a weight would be 2^4 or more (fp16 holds those below 2^16)
-                    float y[2][NB][4];
+                    // -- 2^(s - m) (times the scale when there is one per key): s is
+                    //    kept for the case that m moves
+                    float w[2][NB][4], lt[NB][2];
                     bool raise = false;
+                    auto weights = [&]() {
 #pragma unroll
-                    for (int rc = 0; rc < 2; ++rc)
+                        for (int nb = 0; nb < NB; ++nb) lt[nb][0] = lt[nb][1] = 0.0f;
 #pragma unroll
-                        for (int nb = 0; nb < NB; ++nb)
+                        for (int rc = 0; rc < 2; ++rc)
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                y[rc][nb][c] = s[rc][nb][c] - nm[nb][c & 1];
-                                raise |= y[rc][nb][c] > 4.0f - vl[rc][c >> 1];
+                            for (int x = 0; x < 2; ++x) {
+                                float f = vs[rc][0][x];
+#pragma unroll
+                                for (int gr = 1; gr < NG; ++gr) f = fmaxf(f, vs[rc][gr][x]);
+                                f *= vf;
+#pragma unroll
+                                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                                    for (int c = 0; c < 2; ++c) {
+                                        const float q = ex2(s[rc][nb][2 * x + c] - m[nb][c]);
+                                        lt[nb][c] += q;
+                                        raise |= q * f >= 4096.0f;
+                                        w[rc][nb][2 * x + c] = NG == 1 ? q * f : q * vf;
+                                    }
                             }
+                    };
+                    weights();
                     if (__any_sync(0xFFFFFFFFu, raise)) {
+                        float fm[NB][2], top = 0.0f;
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                             for (int c = 0; c < 2; ++c) {
-                                float d = fmaxf(fmaxf(s[0][nb][c] + vl[0][0], s[0][nb][c + 2] + vl[0][1]),
-                                                fmaxf(s[1][nb][c] + vl[1][0], s[1][nb][c + 2] + vl[1][1]));
+                                float d = fmaxf(fmaxf(s[0][nb][c], s[0][nb][c + 2]),
+                                                fmaxf(s[1][nb][c], s[1][nb][c + 2]));
 #pragma unroll
                                 for (int o = 4; o < 32; o <<= 1)
                                     d = fmaxf(d, __shfl_xor_sync(0xFFFFFFFFu, d, o));
-                                d = fmaxf(d, nm[nb][c]);
-                                const float fo = ex2(nm[nb][c] - d);
-                                nm[nb][c] = d;
-                                l[nb][c] *= fo;
+                                d = fmaxf(d, m[nb][c]);
+                                fm[nb][c] = ex2(m[nb][c] - d);
+                                m[nb][c] = d;
 #pragma unroll
-                                for (int rc = 0; rc < 2; ++rc) {
-                                    y[rc][nb][c] = s[rc][nb][c] - d;
-                                    y[rc][nb][c + 2] = s[rc][nb][c + 2] - d;
-                                }
+                                for (int rc = 0; rc < 2; ++rc)
+#pragma unroll
+                                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                                        for (int gr = 0; gr < NG; ++gr)
+                                            top = fmaxf(top, ex2(s[rc][nb][2 * x + c] - d) * vs[rc][gr][x]);
+                            }
+                        // the largest weight (all are >= 0: their bits order them)
+                        const uint32_t tb = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top));
+                        const int e = max(ve, min(max((int)(tb >> 23) - 127, -100), 100));
+                        const float fe = ve == kNoExp ? 1.0f : ex2((float)(ve - e));
+                        ve = e;
+                        vf = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                l[nb][c] *= fm[nb][c];
 #pragma unroll
                                 for (int z = 0; z < 4 * VW; ++z) {
-                                    acc[z][nb][c] *= fo;
-                                    acc[z][nb][c + 2] *= fo;
+                                    acc[z][nb][c] *= fm[nb][c] * fe;
+                                    acc[z][nb][c + 2] *= fm[nb][c] * fe;
                                 }
                             }
+                        weights();
                     }
-                    // -- weights, values: rows d, columns 2 tig, 2 tig + 1
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {
+                        l[nb][0] += lt[nb][0];
+                        l[nb][1] += lt[nb][1];
+                    }
+                    // -- values: rows d, columns 2 tig, 2 tig + 1
 #pragma unroll
                     for (int rc = 0; rc < 2; ++rc) {
                         const uint8_t *st = sr[rc];
@@ -1131,16 +1155,13 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                const float p0 = ex2(y[rc][nb][2 * x]);
-                                const float p1 = ex2(y[rc][nb][2 * x + 1]);
-                                l[nb][0] += p0;
-                                l[nb][1] += p1;
+                            for (int x = 0; x < 2; ++x)
 #pragma unroll
-                                for (int gr = 0; gr < NG; ++gr)
+                                for (int gr = 0; gr < NG; ++gr) {
+                                    const float f = NG == 1 ? 1.0f : vs[rc][gr][x];
                                     wf[gr][nb][x] = transpose8(
-                                        pack_f16x2(p0 * vs[rc][gr][x], p1 * vs[rc][gr][x]));
-                            }
+                                        pack_f16x2(w[rc][nb][2 * x] * f, w[rc][nb][2 * x + 1] * f));
+                                }
                         uint32_t vw[2][KW];
 #pragma unroll
                         for (int q = 0; q < (2 * KW + 3) / 4; ++q) {
@@ -1198,6 +1219,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
             // ends inside it (the ring goes on to serve)
             const bool whole = u == item_begin && seg_end == item_end;
             const int which = whole || seg_end == w_end ? 1 : 0;
+            const float back = ve == kNoExp ? 0.0f : __uint_as_float((uint32_t)(127 + ve) << 23);   // 2^E
             float *slot = reinterpret_cast<float *>(
                 smem + (which ? L::ring_off + warp * L::ring : L::first_off + warp * L::slot));
 #pragma unroll
@@ -1209,7 +1231,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
                     if (gid == 0) {
-                        slot[SL::stats + row] = nm[nb][c];
+                        slot[SL::stats + row] = m[nb][c];
                         slot[SL::stats + R + row] = t;
                     }
 #pragma unroll
@@ -1219,7 +1241,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
 #pragma unroll
                             for (int hi = 0; hi < 2; ++hi)
                                 slot[row * SL::pitch + 64 * wi + 16 * nib + 8 * hi + gid] =
-                                    acc[4 * wi + nib][nb][2 * hi + c];
+                                    acc[4 * wi + nib][nb][2 * hi + c] * back;
                 }
             if (whole) {
                 __syncwarp();
