@@ -193,7 +193,7 @@ QZ_API qz_status qz_workspace_bytes(int32_t op, int64_t M, int64_t N, int64_t K,
         const qz_status s = check_gemv_shape(M, N, K);
         if (s != QZ_OK) return s;
         *bytes = lora_gemv_bytes(op == QZ_OP_W4A16_LORA_GEMV ? 4 : 8, M, N, K, group_size) +
-                 lora_scratch_bytes(M, N);
+                 lora_scratch_bytes(M);
         return QZ_OK;
     }
     case QZ_OP_KV4_ATTENTION:
@@ -488,21 +488,20 @@ qz_status lora_gemv(int bits, const void *a, const void *codes, const void *scal
         !aligned(lora_scales, 4))
         return QZ_ERR_ALIGNMENT;
     const size_t base = lora_gemv_bytes(bits, M, N, K, group_size);
-    qz_status s = check_workspace(base + lora_scratch_bytes(M, N), workspace, workspace_bytes);
+    qz_status s = check_workspace(base + lora_scratch_bytes(M), workspace, workspace_bytes);
     if (s != QZ_OK) return s;
     const GemvPlan plan =
         bits == 4 ? gemv_plan(M, N, K, 4, device_sm_count(),
                               gemv_unit_k(4, M, N, K, group_size, scales, zeros))
                   : gemv_plan(M, N, K, 8, device_sm_count());
-    const float *delta = nullptr;
-    s = launch_lora(a, lora_a, lora_b, adapters, lora_scales, n_adapters, rank, M, N, K,
-                    static_cast<char *>(workspace) + base, &delta, st);
+    LoraUp up;
+    s = launch_lora(a, lora_a, lora_b, adapters, lora_scales, n_adapters, rank, M, K,
+                    static_cast<char *>(workspace) + base, &up, st);
     if (s != QZ_OK) return s;
-    // The GEMV always overlaps the adapters' kernels (mode 1 of
-    // qz_set_launch_overlap): they do not write the weights, and the first of
-    // them starts only after whatever was queued before this call.
-    return launch_gemv_add(bits, a, codes, scales, zeros, M, N, K, group_size, delta, y, workspace,
-                           plan, 1, st);
+    // The GEMV overlaps the kernel that makes h, which writes nothing else that
+    // it reads and starts only after whatever was queued before this call.
+    return launch_gemv_lora(bits, a, codes, scales, zeros, M, N, K, group_size, up, y, workspace,
+                            plan, st);
 }
 
 }  // namespace

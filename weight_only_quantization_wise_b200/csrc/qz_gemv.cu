@@ -61,6 +61,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "qz_lora.cuh"
 #include "qz_sm100.cuh"
 
 namespace qz {
@@ -110,26 +111,36 @@ constexpr int kMetaZeroBytes = kTileRows * 16;                 // 16 zeros per r
 // Shared-memory layout (offsets from the 1024-byte aligned base): S stages
 // of [codes | activations (8 MB rows) | gathered scale/zero words], then the
 // two meta slots [scales | zeros], then the barriers.
-template <int BITS, int MB, int META, int FMT = kFmtInt, int HALVES = 1>
+// The adapters in use and their tokens (LORA).
+struct LoraGroups {
+    uint64_t tokens[64];       // of each adapter in use
+    int id[64];
+    int count;
+};
+
+template <int BITS, int MB, int META, int FMT = kFmtInt, int HALVES = 1, bool LORA = false>
 struct Layout {
     static constexpr int code = kCodeStage<BITS> * HALVES;              // code bytes per stage
     static constexpr int act = 8 * MB * kBlockK * HALVES * 2;           // bytes per stage
     static constexpr int stage = code + act + (META == kMetaGather ? kSzStage : 0);
     static constexpr int meta = META == kMetaTma ? 2 * (kMetaScaleBytes + kMetaZeroBytes) : 0;
     static constexpr int lut = FMT == kFmtNv ? 512 : 0;                 // E4M3 -> bf16 table
-    static constexpr int S = (kCtaSmemBudget<MB, HALVES> - meta - lut - 256) / stage;
+    static constexpr int lora = LORA ? 1024 : 0;                        // LoraGroups
+    static constexpr int S = (kCtaSmemBudget<MB, HALVES> - meta - lut - lora - 256) / stage;
     static constexpr uint32_t codes = 0;                                 // + s * stage
     static constexpr uint32_t act_off = code;                            // within a stage
     static constexpr uint32_t sz_off = code + act;                       // within a stage
     static constexpr uint32_t meta_base = S * stage;
     static constexpr uint32_t lut_base = meta_base + meta;
-    static constexpr uint32_t full = lut_base + lut;
+    static constexpr uint32_t lora_base = lut_base + lut;
+    static constexpr uint32_t full = lora_base + lora;
     static constexpr uint32_t empty = full + 8 * S;
     static constexpr uint32_t meta_full = empty + 8 * S;
     static constexpr uint32_t meta_empty = meta_full + 16;
     static constexpr uint32_t abort_flag = meta_empty + 16;
     static constexpr uint32_t end = abort_flag + 16;
     static constexpr uint32_t bytes = end + 1024;                        // + alignment slack
+    static_assert(!LORA || sizeof(LoraGroups) <= lora, "the adapter list fits");
     static_assert(stage % 1024 == 0, "stages keep the 1024-byte alignment of the swizzled codes");
     static_assert(S >= 3, "at least three stages in flight");
     static_assert(end + 1024 <= kCtaSmemBudget<MB, HALVES> + 1024, "the CTAs fit on an SM");
@@ -226,6 +237,14 @@ __device__ __forceinline__ void cp_async_arrive_noinc(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
+// Untiled copy of a contiguous piece of global memory (16-byte multiples).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes,
+                                          uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+        ::"r"(dst), "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar) : "memory");
+}
+
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -305,7 +324,7 @@ struct GemvArgs {
     int bpg_shift;             // log2(group_size / 128) (ring path), else -1
     int kblocks;               // K / 128
     uint16_t *y;
-    const float *addend;       // M x N fp32 added to the sums before the rounding (ADD variants)
+    LoraUp lora;               // adapters' part of the sums (LORA variants)
     float *partials;
     uint32_t *counters;
     int64_t units;             // tasks * kblocks
@@ -607,21 +626,80 @@ __device__ __forceinline__ void gemv_flush(float (&acc)[2][MB][4], const GemvArg
     if (lane == 0) p.counters[sub] = 0u;
 }
 
+// ---- LORA: the adapters' part of a task's sums -----------------------------
+// sum_j B_r[n][j] h_mj, r the adapter of token m, h = hi + lo in bf16.  The rows
+// of B of a task (128 x rank, contiguous) come through the ring as further
+// stages behind the task's units: per adapter in use, 128, 64 or 32 rows at a
+// time, whatever fits a stage.
+template <typename L>
+__device__ __forceinline__ int lora_chunk_rows(int rank) {
+    int rows = kTileRows;
+    while (rows * rank * 2 > L::code + L::act) rows >>= 1;   // 32 rows of 128 ranks: 8 KB
+    return rows;
+}
+// The lines of h, to L1, so that the products below do not wait for each.
+__device__ __forceinline__ void lora_warm(const GemvArgs &p, int lane) {
+    const int bytes = 2 * p.M * p.lora.rank * 2;
+    for (int o = 128 * lane; o < bytes; o += 128 * 32) {
+        uint32_t x;
+        asm volatile("ld.global.ca.u32 %0, [%1];"
+                     : "=r"(x) : "l"(reinterpret_cast<const char *>(p.lora.h) + o) : "memory");
+    }
+}
+// acc (layout as for gemv_flush) += the part of one adapter (tokens `tokens`;
+// columns of other tokens are zero) for the warp's 32 rows of B at `rows`.  A
+// lane reads 16 bytes of a row: ranks 8 t .. 8 t + 7 of every 32.
+template <int MB>
+__device__ __forceinline__ void lora_add(float (&acc)[2][MB][4], const GemvArgs &p, uint32_t rows,
+                                         uint64_t tokens, int lane) {
+    const LoraUp &q = p.lora;
+    const int g = lane >> 2, t = lane & 3;
+    const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 2
+    for (int j = 0; j < q.rank; j += 32) {
+        const bool in = j + 8 * t < q.rank;                  // the rank is a multiple of 8
+        uint4 b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            b[i] = in ? lds128(rows + (uint32_t)(((g + 8 * i) * q.rank + j + 8 * t) * 2)) : none;
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) {
+            if (!((tokens >> (8 * mb)) & 0xFFull)) continue;
+            const int tok = 8 * mb + g;
+            const bool mine = in && ((tokens >> tok) & 1ull);
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+                const uint4 h = mine ? *reinterpret_cast<const uint4 *>(
+                                           q.h + (int64_t)(part * p.M + tok) * q.rank + j + 8 * t)
+                                     : none;
+#pragma unroll
+                for (int rt = 0; rt < 2; ++rt) {
+                    const uint4 x = b[2 * rt], y = b[2 * rt + 1];
+                    dev::mma_bf16_16816(acc[rt][mb], x.x, y.x, x.y, y.y, h.x, h.y);
+                    dev::mma_bf16_16816(acc[rt][mb], x.z, y.z, x.w, y.w, h.z, h.w);
+                }
+            }
+        }
+    }
+}
+
 // The kernel.  META: how int4 scales and zeros arrive (kMetaNone: int8's
 // per-row scales, or int4 groups loaded directly by the consumers).  HALVES:
 // 128-wide K blocks per unit (2: int4 units of 128 rows x 256 k, one
 // 128-byte row of codes per weight row, consumed as two halves).  ACTSW
 // (two-half units): activations as four swizzled 64-k boxes (load_act_sw),
 // else one box of 256 k (one token: its lanes of equal t read the same words).
-// ADD: the sums of a task start from p.addend, in the CTA that covers the
-// task's first K block.
-template <int BITS, int MB, int META, int FMT, int HALVES = 1, bool ACTSW = true, bool ADD = false>
+// LORA: the adapters' second product joins the sums of a task in the CTA that
+// covers the task's first K block, after its last block there.  The launch
+// overlaps the kernel that makes h and waits for it only there (it writes
+// nothing else that this kernel reads).
+template <int BITS, int MB, int META, int FMT, int HALVES = 1, bool ACTSW = true, bool LORA = false>
 __global__ void __launch_bounds__(kThreads, (kCtasPerSm<MB, HALVES>))
 gemv_kernel(const __grid_constant__ CUtensorMap code_map,
             const __grid_constant__ CUtensorMap act_map,
             const __grid_constant__ CUtensorMap scale_map,
             const __grid_constant__ CUtensorMap zero_map, const GemvArgs p) {
-    using L = Layout<BITS, MB, META, FMT, HALVES>;
+    using L = Layout<BITS, MB, META, FMT, HALVES, LORA>;
     static_assert(HALVES == 1 ||
                       (BITS == 4 && MB <= 2 &&
                        (META == kMetaTma || (FMT == kFmtInt && META == kMetaGather))),
@@ -666,6 +744,18 @@ gemv_kernel(const __grid_constant__ CUtensorMap code_map,
                      : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&act_map))
                      : "memory");
+    }
+    LoraGroups *groups = reinterpret_cast<LoraGroups *>(smem + L::lora_base);   // (LORA only)
+    if constexpr (LORA) {
+        if (warp == 0) {
+            int n = 0;
+            for (lora::Groups it(p.lora.ids, p.M, p.lora.adapters, lane); it.next(); ++n)
+                if (lane == 0) {
+                    groups[0].tokens[n] = it.tokens;
+                    groups[0].id[n] = it.id;
+                }
+            if (lane == 0) groups[0].count = n;
+        }
     }
     if (FMT == kFmtNv)        // E4M3 byte -> bf16 bits
         for (int b = threadIdx.x; b < 256; b += blockDim.x)
@@ -720,7 +810,9 @@ gemv_kernel(const __grid_constant__ CUtensorMap code_map,
             }
         };
         bool ok = true;
+        int seg_kb0 = 0;                             // first K block of the task in this CTA
         for (int64_t u = u_begin; u < u_end && ok; ++u) {
+            if (u == u_begin || kb == 0) seg_kb0 = kb;
             if (META == kMetaTma && (u == u_begin || (kb & span_mask) == 0)) {
                 const int m = spans & 1;
                 if (spans >= 2) {
@@ -779,13 +871,42 @@ gemv_kernel(const __grid_constant__ CUtensorMap code_map,
             }
             ++issued;
             if (early_phase) ++no_act;
-            if (++kb == KB) {
-                kb = 0;
-                ++task;
-            }
             if (++s == S) {
                 s = 0;
                 ++r;
+            }
+            if constexpr (LORA) {
+                if (seg_kb0 == 0 && (kb + 1 == KB || u + 1 == u_end)) {
+                    // the task's rows of B, adapter by adapter
+                    const int cr = lora_chunk_rows<L>(p.lora.rank), rb = 2 * p.lora.rank;
+                    for (int c = 0; c < groups[0].count * (kTileRows / cr) && ok; ++c) {
+                        const int gi = c / (kTileRows / cr);
+                        const int row0 = task * kTileRows + c % (kTileRows / cr) * cr;
+                        if (r > 0 && !mbar_wait(empty_bar(s), (r - 1) & 1, p.wait_limit, abort_flag,
+                                                p.err_word)) {
+                            ok = false;
+                            break;
+                        }
+                        if (lane == 0) {
+                            const int rows = max(0, min(cr, p.N - row0));
+                            mbar_arrive_expect_tx(full_bar(s), (uint32_t)(rows * rb));
+                            if (rows > 0)
+                                bulk_load(stage_addr(s),
+                                          p.lora.up + ((int64_t)groups[0].id[gi] * p.N + row0) * p.lora.rank,
+                                          (uint32_t)(rows * rb), full_bar(s));
+                        }
+                        if (META == kMetaGather) cp_async_arrive_noinc(full_bar(s));
+                        ++issued;
+                        if (++s == S) {
+                            s = 0;
+                            ++r;
+                        }
+                    }
+                }
+            }
+            if (++kb == KB) {
+                kb = 0;
+                ++task;
             }
         }
         finish_early();                              // ranges shorter than the ring
@@ -836,22 +957,6 @@ gemv_kernel(const __grid_constant__ CUtensorMap code_map,
                 for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) acc[c][rt][mb][j] = 0.0f;
-        if constexpr (ADD) {
-            if (kb0 == 0) {
-#pragma unroll
-                for (int rt = 0; rt < 2; ++rt)
-#pragma unroll
-                    for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int row = n0 + 16 * rt + g + 8 * (j >> 1);
-                            const int tok = 8 * mb + 2 * t + (j & 1);
-                            if (row < p.N && tok < p.M)
-                                acc[0][rt][mb][j] = __ldcg(p.addend + (int64_t)tok * p.N + row);
-                        }
-            }
-        }
-
         for (int kb = kb0; kb < kb_end; ++kb) {
             int m = 0;
             if (META == kMetaTma) {
@@ -1054,6 +1159,26 @@ gemv_kernel(const __grid_constant__ CUtensorMap code_map,
                 for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) acc[0][rt][mb][j] += acc[c][rt][mb][j];
+        if constexpr (LORA) {
+            if (kb0 == 0) {
+                wait_for_previous_grid();                    // h
+                lora_warm(p, lane);
+                const int cr = lora_chunk_rows<L>(p.lora.rank), per = kTileRows / cr;
+                for (int c = 0; c < groups[0].count * per; ++c) {
+                    if (!mbar_wait(full_bar(s), r & 1, p.wait_limit, abort_flag, p.err_word)) return;
+                    if (w * kRowsPerWarp / cr == c % per)
+                        lora_add<MB>(acc[0], p,
+                                     stage_addr(s) + (uint32_t)(w * kRowsPerWarp % cr * p.lora.rank * 2),
+                                     groups[0].tokens[c / per], lane);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(empty_bar(s));
+                    if (++s == S) {
+                        s = 0;
+                        ++r;
+                    }
+                }
+            }
+        }
         gemv_flush<MB>(acc[0], p, task, w, nkb == KB, cta, lane,
                        FMT == kFmtNv ? __ldg(p.tensor_scale) : 1.0f);
         u += nkb;
@@ -1073,10 +1198,10 @@ struct Maps {
     CUtensorMap code, act, scale, zero;
 };
 
-template <int BITS, int MB, int META, int FMT, int HALVES = 1, bool ACTSW = true, bool ADD = false>
+template <int BITS, int MB, int META, int FMT, int HALVES = 1, bool ACTSW = true, bool LORA = false>
 qz_status launch_variant(const Maps &maps, const GemvArgs &args, dim3 grid, int overlap,
                          cudaStream_t st) {
-    constexpr int smem = Layout<BITS, MB, META, FMT, HALVES>::bytes;
+    constexpr int smem = Layout<BITS, MB, META, FMT, HALVES, LORA>::bytes;
     static DeviceOnce attr_once;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) {
@@ -1084,13 +1209,13 @@ qz_status launch_variant(const Maps &maps, const GemvArgs &args, dim3 grid, int 
         return QZ_ERR_CUDA;
     }
     if (attr_once.run(dev, [] {
-            cudaError_t e = cudaFuncSetAttribute(gemv_kernel<BITS, MB, META, FMT, HALVES, ACTSW, ADD>,
+            cudaError_t e = cudaFuncSetAttribute(gemv_kernel<BITS, MB, META, FMT, HALVES, ACTSW, LORA>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  smem);
             // three rings per SM need (nearly) all of the unified memory as
             // shared memory
             if (e == cudaSuccess)
-                e = cudaFuncSetAttribute(gemv_kernel<BITS, MB, META, FMT, HALVES, ACTSW, ADD>,
+                e = cudaFuncSetAttribute(gemv_kernel<BITS, MB, META, FMT, HALVES, ACTSW, LORA>,
                                          cudaFuncAttributePreferredSharedMemoryCarveout, 100);
             return e;
         }) != cudaSuccess)
@@ -1105,21 +1230,21 @@ qz_status launch_variant(const Maps &maps, const GemvArgs &args, dim3 grid, int 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = overlap > 0 ? 1 : 0;
-    cudaLaunchKernelEx(&cfg, gemv_kernel<BITS, MB, META, FMT, HALVES, ACTSW, ADD>, maps.code, maps.act,
+    cudaLaunchKernelEx(&cfg, gemv_kernel<BITS, MB, META, FMT, HALVES, ACTSW, LORA>, maps.code, maps.act,
                        maps.scale, maps.zero, args);
     return launch_status();
 }
 
-template <int BITS, int META, int FMT = kFmtInt, bool ADD = false>
+template <int BITS, int META, int FMT = kFmtInt, bool LORA = false>
 qz_status launch_mb(const Maps &maps, const GemvArgs &args, dim3 grid, int overlap,
                     cudaStream_t st) {
     if (args.M <= 8)
-        return launch_variant<BITS, 1, META, FMT, 1, true, ADD>(maps, args, grid, overlap, st);
+        return launch_variant<BITS, 1, META, FMT, 1, true, LORA>(maps, args, grid, overlap, st);
     if (args.M <= 16 || FMT != kFmtInt)
-        return launch_variant<BITS, 2, META, FMT, 1, true, ADD>(maps, args, grid, overlap, st);
+        return launch_variant<BITS, 2, META, FMT, 1, true, LORA>(maps, args, grid, overlap, st);
     if (args.M <= 32)
-        return launch_variant<BITS, 4, META, kFmtInt, 1, true, ADD>(maps, args, grid, overlap, st);
-    return launch_variant<BITS, 8, META, kFmtInt, 1, true, ADD>(maps, args, grid, overlap, st);
+        return launch_variant<BITS, 4, META, kFmtInt, 1, true, LORA>(maps, args, grid, overlap, st);
+    return launch_variant<BITS, 8, META, kFmtInt, 1, true, LORA>(maps, args, grid, overlap, st);
 }
 
 // How the int4 GEMV's scales and zeros reach shared memory: as TMA tiles
@@ -1147,11 +1272,11 @@ bool two_half_ok(int64_t M, int64_t N, int64_t K, int64_t group_size, const void
     return meta == kMetaGather && (group_size > kBlockK || (K / group_size) % 2 == 0);
 }
 
-template <int BITS, bool ADD = false>
+template <int BITS, bool LORA = false>
 qz_status launch_gemv(const void *a, const void *codes, const void *scales, const void *zeros,
                       int64_t M, int64_t N, int64_t K, int64_t group_size, void *y,
                       void *workspace, const GemvPlan &plan, int overlap, cudaStream_t st,
-                      const float *addend = nullptr) {
+                      const LoraUp *up = nullptr) {
     GemvArgs args;
     args.scales = static_cast<const uint16_t *>(scales);
     args.fp4_scales = nullptr;
@@ -1168,7 +1293,7 @@ qz_status launch_gemv(const void *a, const void *codes, const void *scales, cons
     args.meta_span_shift = args.bpg_shift >= 0 ? args.bpg_shift + 3 - (halves - 1) : 0;
     args.kblocks = (int)(K / plan.unit_k);
     args.y = static_cast<uint16_t *>(y);
-    args.addend = addend;
+    args.lora = LORA ? *up : LoraUp{};
     args.partials = nullptr;
     args.counters = nullptr;
     if (plan.total_bytes > 0) {
@@ -1179,7 +1304,7 @@ qz_status launch_gemv(const void *a, const void *codes, const void *scales, cons
     args.units = plan.tasks * plan.kblocks;
     args.ctas = plan.ctas;
     args.slots = (int)plan.slots;
-    args.prefetch_early = overlap;
+    args.prefetch_early = LORA ? 0 : overlap;      // LORA waits for h alone
     args.wait_limit = device_wait_limit();
     args.err_word = device_error_word();
     if (args.err_word == nullptr) return QZ_ERR_CUDA;
@@ -1216,29 +1341,29 @@ qz_status launch_gemv(const void *a, const void *codes, const void *scales, cons
                                     CU_TENSOR_MAP_SWIZZLE_NONE))
                 return QZ_ERR_CUDA;
             if (halves == 2)
-                return M == 1   ? launch_variant<4, 1, kMetaTma, kFmtInt, 2, false, ADD>(maps, args, grid,
+                return M == 1   ? launch_variant<4, 1, kMetaTma, kFmtInt, 2, false, LORA>(maps, args, grid,
                                                                                    overlap, st)
-                       : M <= 8 ? launch_variant<4, 1, kMetaTma, kFmtInt, 2, true, ADD>(maps, args, grid,
+                       : M <= 8 ? launch_variant<4, 1, kMetaTma, kFmtInt, 2, true, LORA>(maps, args, grid,
                                                                           overlap, st)
-                              : launch_variant<4, 2, kMetaTma, kFmtInt, 2, true, ADD>(maps, args, grid,
+                              : launch_variant<4, 2, kMetaTma, kFmtInt, 2, true, LORA>(maps, args, grid,
                                                                           overlap, st);
-            return launch_mb<4, kMetaTma, kFmtInt, ADD>(maps, args, grid, overlap, st);
+            return launch_mb<4, kMetaTma, kFmtInt, LORA>(maps, args, grid, overlap, st);
         }
         // The gather path copies the aligned 4-byte words holding each scale
         // and zero.
         if (meta == kMetaGather) {
             if (halves == 2)
-                return M == 1   ? launch_variant<4, 1, kMetaGather, kFmtInt, 2, false, ADD>(maps, args, grid,
+                return M == 1   ? launch_variant<4, 1, kMetaGather, kFmtInt, 2, false, LORA>(maps, args, grid,
                                                                                    overlap, st)
-                       : M <= 8 ? launch_variant<4, 1, kMetaGather, kFmtInt, 2, true, ADD>(maps, args, grid,
+                       : M <= 8 ? launch_variant<4, 1, kMetaGather, kFmtInt, 2, true, LORA>(maps, args, grid,
                                                                           overlap, st)
-                              : launch_variant<4, 2, kMetaGather, kFmtInt, 2, true, ADD>(maps, args, grid,
+                              : launch_variant<4, 2, kMetaGather, kFmtInt, 2, true, LORA>(maps, args, grid,
                                                                              overlap, st);
-            return launch_mb<4, kMetaGather, kFmtInt, ADD>(maps, args, grid, overlap, st);
+            return launch_mb<4, kMetaGather, kFmtInt, LORA>(maps, args, grid, overlap, st);
         }
-        return launch_mb<4, kMetaNone, kFmtInt, ADD>(maps, args, grid, overlap, st);
+        return launch_mb<4, kMetaNone, kFmtInt, LORA>(maps, args, grid, overlap, st);
     } else {
-        return launch_mb<8, kMetaNone, kFmtInt, ADD>(maps, args, grid, overlap, st);
+        return launch_mb<8, kMetaNone, kFmtInt, LORA>(maps, args, grid, overlap, st);
     }
 }
 
@@ -1406,15 +1531,15 @@ qz_status launch_w8a16_gemv(const void *a, const void *codes, const void *scales
                           st);
 }
 
-qz_status launch_gemv_add(int bits, const void *a, const void *codes, const void *scales,
-                          const void *zeros, int64_t M, int64_t N, int64_t K, int64_t group_size,
-                          const float *addend, void *y, void *workspace, const GemvPlan &plan,
-                          int overlap, cudaStream_t st) {
+qz_status launch_gemv_lora(int bits, const void *a, const void *codes, const void *scales,
+                           const void *zeros, int64_t M, int64_t N, int64_t K, int64_t group_size,
+                           const LoraUp &up, void *y, void *workspace, const GemvPlan &plan,
+                           cudaStream_t st) {
     if (bits == 4)
         return launch_gemv<4, true>(a, codes, scales, zeros, M, N, K, group_size, y, workspace,
-                                    plan, overlap, st, addend);
-    return launch_gemv<8, true>(a, codes, scales, nullptr, M, N, K, K, y, workspace, plan, overlap,
-                                st, addend);
+                                    plan, 1, st, &up);
+    return launch_gemv<8, true>(a, codes, scales, nullptr, M, N, K, K, y, workspace, plan, 1, st,
+                                &up);
 }
 
 }  // namespace qz

@@ -130,21 +130,24 @@ qz_status launch_w8a16_gemv(const void *a, const void *codes, const void *scales
                             int64_t M, int64_t N, int64_t K, void *y, void *workspace,
                             const GemvPlan &plan, int overlap, cudaStream_t stream);
 
-// The integer GEMVs with an M x N fp32 addend under the sums (qz_gemv.cu).
-qz_status launch_gemv_add(int bits, const void *a, const void *codes, const void *scales,
-                          const void *zeros, int64_t M, int64_t N, int64_t K, int64_t group_size,
-                          const float *addend, void *y, void *workspace, const GemvPlan &plan,
-                          int overlap, cudaStream_t stream);
-
-// Low-rank adapters beside a packed projection (qz_lora.cu): writes the
-// adapters' part of y to an M x N fp32 array in `scratch`
-// (lora_scratch_bytes) and returns its place.
+// Low-rank adapters beside a packed projection: launch_lora (qz_lora.cu) makes
+// the first product h in `scratch` (lora_scratch_bytes), launch_gemv_lora
+// (qz_gemv.cu) is the integer GEMV that adds the second one to its sums.
 constexpr int64_t kLoraMaxRank = 128;
-size_t lora_scratch_bytes(int64_t M, int64_t N);
+struct LoraUp {
+    const uint16_t *up;        // adapters x N x rank
+    const uint16_t *h;         // [2][M][rank]: bf16 hi, lo
+    const int32_t *ids;        // adapter of each token
+    int rank, adapters;
+};
+size_t lora_scratch_bytes(int64_t M);
 qz_status launch_lora(const void *a, const void *lora_a, const void *lora_b, const void *adapters,
                       const void *lora_scales, int64_t n_adapters, int64_t rank, int64_t M,
-                      int64_t N, int64_t K, void *scratch, const float **delta,
-                      cudaStream_t stream);
+                      int64_t K, void *scratch, LoraUp *up, cudaStream_t stream);
+qz_status launch_gemv_lora(int bits, const void *a, const void *codes, const void *scales,
+                           const void *zeros, int64_t M, int64_t N, int64_t K, int64_t group_size,
+                           const LoraUp &up, void *y, void *workspace, const GemvPlan &plan,
+                           cudaStream_t stream);
 
 // FP4 with block scales (qz_fp4.cu, qz_gemv.cu, qz_gemm_fp4.cu); kind 0 =
 // MXFP4, 1 = NVFP4.

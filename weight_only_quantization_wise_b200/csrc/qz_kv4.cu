@@ -922,19 +922,11 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                     qsum[gr][nb][1] = __shfl_sync(0xFFFFFFFFu, t, 8 * tig + 4);
                 }
             }
-            // keys each column's row may see: [klo, khi)
-            int khi[NB][2], klo[NB][2];
+            // keys that all rows, and that any row, of the tile may see
             const int pos0 = sw.len - sw.n;
             const int r0 = rt * R, r1 = min(r0 + R, sw.n * p.share) - 1;
             const int all_hi = pos0 + r0 / p.share + 1, any_hi = pos0 + r1 / p.share + 1;
             const int all_lo = p.window > 0 ? max(any_hi, 0) - p.window : 0;
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    khi[nb][c] = pos0 + min(r0 + 8 * nb + 2 * tig + c, r1) / p.share + 1;
-                    klo[nb][c] = p.window > 0 ? max(khi[nb][c], 0) - p.window : 0;
-                }
 
             // ---- main loop ----
             float acc[4 * VW][NB][4], l[NB][2], m[NB][2], vf = 1.0f;
@@ -1056,6 +1048,15 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                             for (int rc = 0; rc < 2; ++rc)      // existing keys without a page
                                 if (!((got >> rc) & 1u) && 2 * i + rc < nblk && key0 + 16 * rc < sw.len)
                                     atomicOr(p.err_word, kErrIndex);
+                        // keys each column's row may see: [klo, khi)
+                        int khi[NB][2], klo[NB][2];
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                khi[nb][c] = pos0 + min(r0 + 8 * nb + 2 * tig + c, r1) / p.share + 1;
+                                klo[nb][c] = p.window > 0 ? max(khi[nb][c], 0) - p.window : 0;
+                            }
 #pragma unroll
                         for (int rc = 0; rc < 2; ++rc)
 #pragma unroll
