@@ -641,7 +641,7 @@ __device__ __forceinline__ int lora_chunk_rows(int rank) {
 __device__ __forceinline__ void lora_warm(const GemvArgs &p, int lane) {
     const int bytes = 2 * p.M * p.lora.rank * 2;
     for (int o = 128 * lane; o < bytes; o += 128 * 32) {
-        uint32_t x;
+        [[maybe_unused]] uint32_t x;
         asm volatile("ld.global.ca.u32 %0, [%1];"
                      : "=r"(x) : "l"(reinterpret_cast<const char *>(p.lora.h) + o) : "memory");
     }
@@ -655,30 +655,51 @@ __device__ __forceinline__ void lora_add(float (&acc)[2][MB][4], const GemvArgs 
     const LoraUp &q = p.lora;
     const int g = lane >> 2, t = lane & 3;
     const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll 2
-    for (int j = 0; j < q.rank; j += 32) {
-        const bool in = j + 8 * t < q.rank;                  // the rank is a multiple of 8
-        uint4 b[4];
+    for (int j = 0; j < q.rank; j += 64) {                   // 64 ranks' loads together
+        bool in[2];                                          // the rank is a multiple of 8
+        uint4 b[2][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            b[i] = in ? lds128(rows + (uint32_t)(((g + 8 * i) * q.rank + j + 8 * t) * 2)) : none;
+        for (int x = 0; x < 2; ++x) {
+            in[x] = j + 32 * x + 8 * t < q.rank;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                b[x][i] = in[x] ? lds128(rows + (uint32_t)(((g + 8 * i) * q.rank + j + 32 * x + 8 * t) * 2))
+                                : none;
+        }
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb) {
             if (!((tokens >> (8 * mb)) & 0xFFull)) continue;
             const int tok = 8 * mb + g;
-            const bool mine = in && ((tokens >> tok) & 1ull);
+            const bool mine = (tokens >> tok) & 1ull;
+            uint4 h[2][2];
 #pragma unroll
-            for (int part = 0; part < 2; ++part) {
-                const uint4 h = mine ? *reinterpret_cast<const uint4 *>(
-                                           q.h + (int64_t)(part * p.M + tok) * q.rank + j + 8 * t)
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+                    h[x][part] = mine && in[x]
+                                     ? *reinterpret_cast<const uint4 *>(
+                                           q.h + (int64_t)(part * p.M + tok) * q.rank + j + 32 * x + 8 * t)
                                      : none;
+            // four chains of products: hi and lo of the two 32s
+            float sum[2][2][2][4] = {};
 #pragma unroll
-                for (int rt = 0; rt < 2; ++rt) {
-                    const uint4 x = b[2 * rt], y = b[2 * rt + 1];
-                    dev::mma_bf16_16816(acc[rt][mb], x.x, y.x, x.y, y.y, h.x, h.y);
-                    dev::mma_bf16_16816(acc[rt][mb], x.z, y.z, x.w, y.w, h.z, h.w);
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                    if (x == 1 && j + 32 >= q.rank) continue;
+#pragma unroll
+                    for (int rt = 0; rt < 2; ++rt) {
+                        const uint4 u = b[x][2 * rt], v = b[x][2 * rt + 1], y = h[x][part];
+                        dev::mma_bf16_16816(sum[x][part][rt], u.x, v.x, u.y, v.y, y.x, y.y);
+                        dev::mma_bf16_16816(sum[x][part][rt], u.z, v.z, u.w, v.w, y.z, y.w);
+                    }
                 }
-            }
+#pragma unroll
+            for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[rt][mb][i] += (sum[0][0][rt][i] + sum[1][0][rt][i]) +
+                                      (sum[0][1][rt][i] + sum[1][1][rt][i]);
         }
     }
 }

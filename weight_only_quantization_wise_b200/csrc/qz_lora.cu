@@ -6,7 +6,8 @@
 // Tokens that share an adapter are worked on together, so each adapter in use
 // is read once: every warp finds the adapters and their tokens from the M
 // indices itself (qz_lora.cuh).  The product runs on mma.sync m16n8k16 with
-// bf16 operands and fp32 sums: 16 ranks x 8 tokens.  The fragments' k order is
+// bf16 operands and fp32 sums: 16 ranks x 8 tokens, up
+// to 16 tokens at a time.  The fragments' k order is
 // free as long as both operands agree, so a lane reads 16 consecutive bytes of
 // a row: k = 8 tid .. 8 tid + 7 of every 32.  A cluster of 8 blocks takes 16
 // ranks of one adapter; the blocks and their 8 warps share K, and their sums
@@ -24,6 +25,7 @@ namespace {
 constexpr unsigned kErrIndex = 2u;     // bit of the device error word: adapter index out of range
 constexpr int kDownWarps = 8;
 constexpr int kCluster = 8;
+static_assert(32 * kDownWarps == 16 * 16, "a thread per rank and token");
 
 struct LoraArgs {
     const uint16_t *a, *down;          // M x K; adapters x R x K
@@ -68,15 +70,15 @@ __device__ __forceinline__ void cluster_sync() {
 __global__ void __launch_bounds__(32 * kDownWarps) __cluster_dims__(1, 1, kCluster)
 lora_down_kernel(const LoraArgs p) {
     grid_release();
-    __shared__ float part[kDownWarps][16 * 8], sums[16 * 8];
+    __shared__ float part[kDownWarps][16 * 16], sums[16 * 16];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
     const int j0 = 16 * blockIdx.y, rank = blockIdx.z;
     if (blockIdx.x == 0 && j0 == 0 && rank == 0 && threadIdx.x < p.M &&
         p.ids[threadIdx.x] >= p.adapters)
         atomicOr(p.err_word, kErrIndex);
     lora::Groups it(p.ids, p.M, p.adapters, lane);
-    for (unsigned i = 0; i <= blockIdx.x; ++i)
-        if (!it.next()) return;                              // the whole cluster
+    it.skip(blockIdx.x);
+    if (!it.next()) return;                                  // the whole cluster
     const int id = it.id;
     uint64_t mask = it.tokens;
     const float scale = p.scales[id];
@@ -88,37 +90,46 @@ lora_down_kernel(const LoraArgs p) {
     const int s0 = w * steps / (kCluster * kDownWarps), s1 = (w + 1) * steps / (kCluster * kDownWarps);
     const uint4 none = make_uint4(0u, 0u, 0u, 0u);
     while (mask) {
-        const int tok = nth_token(mask, gid);                // column gid
-        const uint16_t *act = p.a + (int64_t)(tok < 0 ? 0 : tok) * p.K + 8 * tid;
+        const bool two = __popcll(mask) > 8;
+        const int tok0 = nth_token(mask, gid), tok1 = nth_token(mask, gid + 8);   // columns gid, gid + 8
+        const uint16_t *act0 = p.a + (int64_t)max(tok0, 0) * p.K + 8 * tid;
+        const uint16_t *act1 = p.a + (int64_t)max(tok1, 0) * p.K + 8 * tid;
         float acc[2][4] = {};
 #pragma unroll 4
         for (int s = s0; s < s1; ++s) {
             const uint4 x = v0 ? dev::ld_stream_v4(row0 + 32 * s) : none;
             const uint4 y = v1 ? dev::ld_stream_v4(row1 + 32 * s) : none;
-            const uint4 b = tok >= 0 ? __ldg(reinterpret_cast<const uint4 *>(act + 32 * s)) : none;
+            const uint4 b = tok0 >= 0 ? __ldg(reinterpret_cast<const uint4 *>(act0 + 32 * s)) : none;
             dev::mma_bf16_16816(acc[0], x.x, y.x, x.y, y.y, b.x, b.y);
-            dev::mma_bf16_16816(acc[1], x.z, y.z, x.w, y.w, b.z, b.w);
+            dev::mma_bf16_16816(acc[0], x.z, y.z, x.w, y.w, b.z, b.w);
+            if (two) {
+                const uint4 c = tok1 >= 0 ? __ldg(reinterpret_cast<const uint4 *>(act1 + 32 * s)) : none;
+                dev::mma_bf16_16816(acc[1], x.x, y.x, x.y, y.y, c.x, c.y);
+                dev::mma_bf16_16816(acc[1], x.z, y.z, x.w, y.w, c.z, c.w);
+            }
         }
-        // acc[.][i]: rank gid + 8 (i >> 1), token column 2 tid + (i & 1)
+        // acc[c][i]: rank gid + 8 (i >> 1), token column 8 c + 2 tid + (i & 1)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            part[warp][(gid + 8 * (i >> 1)) * 8 + 2 * tid + (i & 1)] = acc[0][i] + acc[1][i];
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                part[warp][(gid + 8 * (i >> 1)) * 16 + 8 * c + 2 * tid + (i & 1)] = acc[c][i];
         __syncthreads();
-        if (threadIdx.x < 128) {
+        {
             float h = 0.0f;
 #pragma unroll
             for (int i = 0; i < kDownWarps; ++i) h += part[i][threadIdx.x];
             sums[threadIdx.x] = h;
         }
         cluster_sync();
-        if (rank == 0 && threadIdx.x < 128) {
+        if (rank == 0) {
             float v[kCluster], h = 0.0f;
 #pragma unroll
             for (int i = 0; i < kCluster; ++i) v[i] = cluster_load(&sums[threadIdx.x], i);
 #pragma unroll
             for (int i = 0; i < kCluster; ++i) h += v[i];
             h *= scale;
-            const int j = j0 + threadIdx.x / 8, t = nth_token(mask, threadIdx.x % 8);
+            const int j = j0 + threadIdx.x / 16, t = nth_token(mask, threadIdx.x % 16);
             if (t >= 0 && j < p.R) {
                 const uint32_t hi = dev::f32_to_bf16_rne(h);
                 p.h[(int64_t)t * p.R + j] = (uint16_t)hi;
@@ -127,7 +138,7 @@ lora_down_kernel(const LoraArgs p) {
             }
         }
         cluster_sync();                                      // sums have been read
-        mask = drop_tokens(mask, 8);
+        mask = drop_tokens(mask, 16);
     }
 }
 

@@ -32,6 +32,7 @@ struct Groups {
         if (M > 32) {
             const uint32_t same_b = __match_any_sync(0xFFFFFFFFu, b);
             bool first_b = b >= 0 && __ffs(same_b) - 1 == lane;
+#pragma unroll
             for (int i = 0; i < 32; ++i) {
                 const int other = __shfl_sync(0xFFFFFFFFu, a, i);
                 if (other == b) first_b = false;
@@ -39,6 +40,10 @@ struct Groups {
             fb = __ballot_sync(0xFFFFFFFFu, first_b);
         }
         firsts = (uint64_t)fb << 32 | fa;
+    }
+    // Leaves out the next n adapters.
+    __device__ __forceinline__ void skip(int n) {
+        for (; n > 0 && firsts; --n) firsts &= firsts - 1;
     }
     __device__ __forceinline__ bool next() {
         if (!firsts) return false;
