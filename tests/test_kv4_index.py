@@ -203,9 +203,11 @@ def test_work_split(ix, case):
         return
     begins = np.cumsum([0] + items)
     quota = ix.s_cta_quota(units, len(items), max(items), grid, min_units, 96)
-    assert quota >= min_units and quota * grid >= units
-    if len(set(items)) == 1 and items[0] <= 96:
-        assert quota >= items[0]
+    assert quota * grid >= units
+    if len(set(items)) == 1 and items[0] <= 96 and len(items) <= grid:
+        assert quota == items[0]                         # whole items
+    else:
+        assert quota >= min_units
     covered, homes, slots, active = 0, {}, {}, 0
     for c in range(grid):
         b0, b1 = ix.s_range_begin(c, quota, units), ix.s_range_begin(c + 1, quota, units)

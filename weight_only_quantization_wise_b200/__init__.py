@@ -669,9 +669,9 @@ def qz_kv4_read(cache, page_table, kv_lens, cu_tokens, tokens, kv_heads, head_di
                              "on the cache's device")
     with _scope(dev, stream):
         if k is None:
-            k = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+            k = cache.new_empty(shape, dtype=torch.bfloat16)
         if v is None:
-            v = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+            v = torch.empty_like(k)
         if tokens == 0:
             return k, v
         status = lib.qz_kv4_read(c, pt, kl, cu, tokens, B, kv_heads, head_dim, page_size,
@@ -694,7 +694,7 @@ def qz_kv4_attention(q, cache, page_table, kv_lens, cu_tokens, kv_heads, page_si
                                                page_size, group_size)
     with _scope(dev, stream):
         if out is None:
-            out = torch.empty((T, H, D), dtype=torch.bfloat16, device=dev)
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
         elif out.shape != q.shape:
             raise ValueError("out must have q's shape")
         if T == 0:

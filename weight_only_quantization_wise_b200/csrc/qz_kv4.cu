@@ -1286,36 +1286,52 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
         return reinterpret_cast<const float *>(
             smem + ((i & 1) ? L::ring_off + (i >> 1) * L::ring : L::first_off + (i >> 1) * L::slot));
     };
-    for (uint32_t todo = heads; todo; todo &= todo - 1) {
+    // CG threads per row, each 16-byte pieces of it; groups of threads that
+    // cover all rows take items in turn
+    constexpr int CG = D / 4 < kThreads / R ? D / 4 : kThreads / R, kGroups = kThreads / (R * CG);
+    constexpr int DI = (D / 4 + CG - 1) / CG;       // pieces per thread
+    const int grp = tid / (R * CG), row = tid % (R * CG) / CG, piece0 = tid % CG;
+    int turn = 0;
+    for (uint32_t todo = heads; todo; todo &= todo - 1, ++turn) {
+        if (grp != turn % kGroups) continue;
         const int i = __ffs(todo) - 1;
         const uint32_t rest = todo & (todo - 1);
         const uint32_t mine = valid & (rest ? (1u << (__ffs(rest) - 1)) - 1u : ~0u) & ~((1u << i) - 1u);
+        const Part &it = parts[i];
+        if (it.rt * R + row >= it.n * p.share) continue;
+        float mx = kNoMax, l = 0.0f;
+        float4 o[DI];
+#pragma unroll
+        for (int y = 0; y < DI; ++y) o[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (uint32_t x = mine; x; x &= x - 1) mx = fmaxf(mx, slot_of(__ffs(x) - 1)[SL::stats + row]);
+        for (uint32_t x = mine; x; x &= x - 1) {
+            const float *q = slot_of(__ffs(x) - 1);
+            const float w = ex2(q[SL::stats + row] - mx);
+            l += w * q[SL::stats + R + row];
+#pragma unroll
+            for (int y = 0; y < DI; ++y) {
+                const int d = 4 * (piece0 + y * CG);
+                if (DI * CG > D / 4 && d >= D) break;
+                const float4 v = *reinterpret_cast<const float4 *>(q + row * SL::pitch + d);
+                o[y].x += w * v.x; o[y].y += w * v.y; o[y].z += w * v.z; o[y].w += w * v.w;
+            }
+        }
         const bool out_of_cta = (shared >> i) & 1u;
         float *part_dst = p.partials + ((int64_t)blockIdx.x * 2 +
-                                        partial_slot(parts[i].item_begin, cta_begin)) * SL::floats;
-        for (int e = tid; e < R * D / 4; e += kThreads) {
-            const int row = e / (D / 4), d = 4 * (e % (D / 4));
-            float n = kNoMax, l = 0.0f;
-            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            for (uint32_t x = mine; x; x &= x - 1) n = fmaxf(n, slot_of(__ffs(x) - 1)[SL::stats + row]);
-            for (uint32_t x = mine; x; x &= x - 1) {
-                const float *q = slot_of(__ffs(x) - 1);
-                const float w = ex2(q[SL::stats + row] - n);
-                const float4 v = *reinterpret_cast<const float4 *>(q + row * SL::pitch + d);
-                l += w * q[SL::stats + R + row];
-                o.x += w * v.x; o.y += w * v.y; o.z += w * v.z; o.w += w * v.w;
-            }
-            if (out_of_cta) {
-                __stcg(reinterpret_cast<float4 *>(part_dst + row * SL::pitch + d), o);
-                if (d == 0) {
-                    __stcg(part_dst + SL::stats + row, n);
-                    __stcg(part_dst + SL::stats + R + row, l);
-                }
-            } else {
-                const Part &it = parts[i];
-                if (uint16_t *dst = out_row<D>(p, it.cu0, it.n, it.h, it.rt * R + row))
-                    store4(dst + d, o, row_factor(l));
-            }
+                                        partial_slot(it.item_begin, cta_begin)) * SL::floats;
+        uint16_t *dst = out_row<D>(p, it.cu0, it.n, it.h, it.rt * R + row);
+        if (out_of_cta && piece0 == 0) {
+            __stcg(part_dst + SL::stats + row, mx);
+            __stcg(part_dst + SL::stats + R + row, l);
+        }
+#pragma unroll
+        for (int y = 0; y < DI; ++y) {
+            const int d = 4 * (piece0 + y * CG);
+            if (DI * CG > D / 4 && d >= D) break;
+            if (out_of_cta)
+                __stcg(reinterpret_cast<float4 *>(part_dst + row * SL::pitch + d), o[y]);
+            else if (dst)
+                store4(dst + d, o[y], row_factor(l));
         }
     }
     if (!shared) return;
@@ -1343,36 +1359,53 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
         const int s0 = partial_slot(it.item_begin, range_begin(c0, quota, units));
         const float *base = p.partials + 2 * c0 * SL::floats;
         auto part = [&](int x) { return base + (int64_t)(2 * x + (x == 0 ? s0 : 0)) * SL::floats; };
-        for (int e = tid; e < R * D / 4; e += kThreads) {
-            const int row = e / (D / 4), d = 4 * (e % (D / 4));
-            // parts in fours, each four's loads together
-            float n = kNoMax, l = 0.0f;
-            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            for (int x0 = 0; x0 < count; x0 += 4) {
-                float pn[4], pl[4];
-                float4 v[4];
+        uint16_t *dst = out_row<D>(p, it.cu0, it.n, it.h, it.rt * R + row);
+        if (grp == k % kGroups && dst) {
+            float mx = kNoMax, l = 0.0f;
+            float4 o[DI];
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const float *q = part(min(x0 + y, count - 1));
-                    pn[y] = __ldcg(q + SL::stats + row);
-                    pl[y] = __ldcg(q + SL::stats + R + row);
-                    v[y] = __ldcg(reinterpret_cast<const float4 *>(q + row * SL::pitch + d));
+            for (int y = 0; y < DI; ++y) o[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            // U parts at a time, their loads together
+            constexpr int U = DI == 1 ? 10 : DI <= 4 ? 4 : 2;
+            for (int x0 = 0; x0 < count; x0 += U) {
+                float pm[U], pl[U];
+                float4 v[U][DI];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const float *q = part(min(x0 + u, count - 1));
+                    pm[u] = __ldcg(q + SL::stats + row);
+                    pl[u] = __ldcg(q + SL::stats + R + row);
+#pragma unroll
+                    for (int y = 0; y < DI; ++y) {
+                        const int d = 4 * min(piece0 + y * CG, D / 4 - 1);
+                        v[u][y] = __ldcg(reinterpret_cast<const float4 *>(q + row * SL::pitch + d));
+                    }
                 }
-                float n2 = n;
+                float m2 = mx;
 #pragma unroll
-                for (int y = 0; y < 4; ++y) n2 = fmaxf(n2, pn[y]);
-                const float f = ex2(n - n2);
-                l *= f; o.x *= f; o.y *= f; o.z *= f; o.w *= f;
-                n = n2;
+                for (int u = 0; u < U; ++u) m2 = fmaxf(m2, pm[u]);
+                const float f = ex2(mx - m2);
+                mx = m2;
+                l *= f;
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const float w = x0 + y < count ? ex2(pn[y] - n) : 0.0f;
-                    l += w * pl[y];
-                    o.x += w * v[y].x; o.y += w * v[y].y; o.z += w * v[y].z; o.w += w * v[y].w;
+                for (int y = 0; y < DI; ++y) { o[y].x *= f; o[y].y *= f; o[y].z *= f; o[y].w *= f; }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const float w = x0 + u < count ? ex2(pm[u] - mx) : 0.0f;
+                    l += w * pl[u];
+#pragma unroll
+                    for (int y = 0; y < DI; ++y) {
+                        o[y].x += w * v[u][y].x; o[y].y += w * v[u][y].y;
+                        o[y].z += w * v[u][y].z; o[y].w += w * v[u][y].w;
+                    }
                 }
             }
-            if (uint16_t *dst = out_row<D>(p, it.cu0, it.n, it.h, it.rt * R + row))
-                store4(dst + d, o, row_factor(l));
+#pragma unroll
+            for (int y = 0; y < DI; ++y) {
+                const int d = 4 * (piece0 + y * CG);
+                if (DI * CG > D / 4 && d >= D) break;
+                store4(dst + d, o[y], row_factor(l));
+            }
         }
         if (tid == 0) p.counters[c0] = 0u;
     }
@@ -1385,16 +1418,17 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
 // 8-row tiles stay in registers (and the rings of 4 groups in shared memory).
 constexpr int kAttnCtasPerSm = 2;      // at most
 template <int D, int NB>
-constexpr int kAttnCtas = D == 256 && NB == 2 ? 1 : kAttnCtasPerSm;
+constexpr int kAttnCtas = (D == 128 && NB == 1) || (D == 256 && NB == 2) ? 1 : kAttnCtasPerSm;
 template <int D, int G, int NB>
-constexpr int kAttnWarps = D == 256 ? (NB == 1 ? 4 : 5) : NB == 2 ? 6 : D / G == 4 ? 7 : 8;
+constexpr int kAttnWarps =
+    D == 256 ? (NB == 1 ? 4 : 5) : NB == 2 ? 6 : D == 64 ? 8 : G == 32 ? 14 : 16;
 
 // Rows of a tile: 8 when a sequence has at most 8 rows per key head on
 // average, else 16 (the keys are read once per tile).
 int attn_tiles(int64_t T, int64_t B, int64_t share) { return T * share <= 8 * B ? 1 : 2; }
 
 template <int D, int G, int NB>
-qz_status launch_attn(const AttnArgs &args, cudaStream_t st) {
+qz_status launch_attn(const AttnArgs &in, cudaStream_t st) {
     constexpr int W = kAttnWarps<D, G, NB>, C = kAttnCtas<D, NB>;
     using L = AttnLayout<D, G, NB, W, C>;
     auto kernel = kv4_attention_kernel<D, G, NB, W, C>;
@@ -1412,6 +1446,11 @@ qz_status launch_attn(const AttnArgs &args, cudaStream_t st) {
             return e;
         }) != cudaSuccess)
         return QZ_ERR_CUDA;
+    // two steps of two blocks per warp at least: with less, a CTA's prologue and
+    // join outweigh its loop (8 warps: 16 and 32 units measured alike, 64 slower)
+    AttnArgs args = in;
+    args.min_units = 4 * W;
+    args.whole_units = 12 * W;                     // a CTA's six steps per warp
     kernel<<<(unsigned)(device_sm_count() * C), 32 * W, L::bytes, st>>>(args);
     return launch_status();
 }
@@ -1541,10 +1580,6 @@ qz_status launch_kv4_attention(const Kv4Cache &c, const void *q, int64_t q_strid
     // counters first: their place does not depend on the tile size
     p.counters = static_cast<uint32_t *>(workspace);
     p.partials = reinterpret_cast<float *>(static_cast<char *>(workspace) + kCounterBytes);
-    // With fewer than 32 blocks a CTA's prologue and join outweigh its loop (16
-    // and 32 measured alike, 64 slower); whole items up to 96 blocks.
-    p.min_units = 32;
-    p.whole_units = 96;
     p.wait_limit = device_wait_limit();
     p.err_word = device_error_word();
     if (p.err_word == nullptr) return QZ_ERR_CUDA;

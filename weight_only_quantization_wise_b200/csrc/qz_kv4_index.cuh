@@ -149,10 +149,9 @@ QZ_HD SeqWork seq_work(int cu0, int cu1, int kv_len, int rows, int capacity, int
 // workspace.
 QZ_HD int64_t cta_quota(int64_t units, int64_t items, int blocks, int64_t ctas, int min_units,
                         int whole_units) {
-    int64_t q = quotient(units + ctas - 1, ctas);
-    if (q < min_units) q = min_units;
-    if (q < blocks && blocks <= whole_units && items * blocks == units) q = blocks;
-    return q;
+    const int64_t q = quotient(units + ctas - 1, ctas);
+    if (q <= blocks && blocks <= whole_units && items * blocks == units) return blocks;
+    return q > min_units ? q : min_units;
 }
 QZ_HD int64_t range_begin(int64_t c, int64_t quota, int64_t units) {
     return c * quota < units ? c * quota : units;
