@@ -308,6 +308,52 @@ def test_strided_heads(dev):
     assert torch.equal(wide[:, 1:], want) and (wide[:, 0] == 0).all()
 
 
+@pytest.mark.parametrize("lens,new", [([40, 3], [2, 1]), ([900], [1])])
+def test_results_at_odd_addresses(dev, lens, new):
+    """An output array that is only 2-byte aligned, with an odd token stride."""
+    H, share, D, g = 1, 3, 64, 64
+    c = Cache(dev, lens, H, D, 16, g)
+    c.append(keys((sum(lens), H, D), 1).to(dev), randn((sum(lens), H, D), 2).to(dev), lens, lens)
+    q = randn((sum(new), share, D), 3).to(dev)
+    want = c.attend(q, lens, new)
+    wide = torch.zeros(sum(new) * 201 + 7, dtype=torch.bfloat16, device=dev)
+    view = wide[7:].view(sum(new), 201)[:, :192].unflatten(1, (share, D))
+    c.attend(q, lens, new, out=view)
+    assert torch.equal(view, want)
+    wide[7:].view(sum(new), 201)[:, :192] = 0
+    assert (wide == 0).all()
+
+
+def test_python_argument_checks(dev):
+    lens = [5, 9]
+    c = Cache(dev, lens, 2, 64, 16, 64)
+    k = randn((14, 2, 64), 1).to(dev)
+    ld, cu = i32(lens, dev), i32([0, 5, 14], dev)
+    good = dict(cache=c.buf, k=k, v=k, page_table=c.table, kv_lens=ld, cu_tokens=cu, page_size=16,
+                group_size=64)
+    qz.qz_kv4_append(**good)
+    for bad in (dict(k=k.float()), dict(k=k[:, :1]), dict(v=k[:5]), dict(k=k.view(14, 128)),
+                dict(k=k.transpose(1, 2)), dict(page_table=c.table.long()), dict(kv_lens=ld[:1]),
+                dict(cu_tokens=cu[:2]), dict(cu_tokens=cu.cpu()), dict(page_table=c.table[0]),
+                dict(cache=c.buf.view(torch.int8)), dict(k=k.cpu(), v=k.cpu()),
+                dict(page_table=c.table[:, ::2])):
+        with pytest.raises(ValueError):
+            qz.qz_kv4_append(**dict(good, **bad))
+    with pytest.raises(ValueError):
+        qz.qz_kv4_attention(k, c.buf, c.table, ld, cu, 2, 16, 64, out=k[:5])
+    with pytest.raises(ValueError):
+        qz.qz_kv4_read(c.buf, c.table, ld, cu, 14, 2, 64, 16, 64, k=k[:5])
+    for bad in (dict(page_size=8), dict(group_size=128), dict(cache=c.buf[:64])):
+        with pytest.raises(qz.QzError):
+            qz.qz_kv4_append(**dict(good, **bad))
+    empty = k[:0]
+    zero = i32([0, 0, 0], dev)
+    qz.qz_kv4_append(c.buf, empty, empty, c.table, ld, zero, 16, 64)
+    assert qz.qz_kv4_attention(empty, c.buf, c.table, ld, zero, 2, 16, 64).shape == empty.shape
+    assert qz.qz_kv4_read(c.buf, c.table, ld, zero, 0, 2, 64, 16, 64)[0].shape == empty.shape
+    assert qz.qz_device_status() == 0
+
+
 def test_results_repeat_and_counters_return_to_zero(dev):
     lens, new = [4000, 900, 17], [1, 3, 1]
     k, v = keys((sum(lens), 2, 128), 1).to(dev), randn((sum(lens), 2, 128), 2).to(dev)

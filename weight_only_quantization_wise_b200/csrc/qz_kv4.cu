@@ -22,11 +22,11 @@ constexpr unsigned kErrIndex = 2u;     // bit of the device error word: bad page
 // append and read
 // ---------------------------------------------------------------------------
 // A unit is one record's worth of tokens: 16 positions (or the part of them
-// that is the call's) of one head.  A warp stages the tokens' 16 x D bf16
-// values and the record in shared memory, so that global memory is read and
-// written in whole rows and whole records; in between a lane works on 64
-// consecutive values of one token ("chunk"), which hold whole groups (or half
-// a group of 128) and whole 32-bit words of K and 16-bit units of V.
+// that is the call's) of one head.  A lane works on 64 consecutive values of
+// one token ("chunk"), which hold whole groups (or half a group of 128) and
+// whole 32-bit words of K and 16-bit units of V; a pass is 32 chunks.  Passes'
+// values and the record go through the warp's shared memory, so that global
+// memory is read and written in whole rows and whole records.
 struct StoreArgs {
     const uint16_t *k, *v;             // append: input
     uint16_t *k_out, *v_out;           // read: output
@@ -40,6 +40,9 @@ struct StoreArgs {
 
 constexpr int kStoreWarps = 4;
 constexpr int kStoreThreads = 32 * kStoreWarps;
+constexpr int kAppendCtas = 4;         // per SM: 128 registers per thread
+template <int D>
+constexpr int kReadCtas = D == 256 ? 4 : 5;        // per SM: 128 or 96 registers per thread
 constexpr int kChunkPitch = 144;       // bytes of a staged chunk: 64 bf16, padded against bank conflicts
 
 template <int D, int G>
@@ -47,8 +50,17 @@ struct StoreLayout {
     static constexpr int NG = D / G;
     static constexpr int chunks = D / 64;                   // of a token
     static constexpr int rec = (int)record_bytes(D, G);
-    static constexpr int tile = 16 * chunks * kChunkPitch;  // one tensor's staged tokens
-    static constexpr int per_warp = 2 * tile + rec;         // K, V, record
+    static constexpr int tile = 32 * kChunkPitch;           // the values of a pass
+    static constexpr int per_warp = tile + rec;
+    static_assert(kReadCtas<D> * (kStoreWarps * per_warp + 4096) <= 228 * 1024, "the CTAs fit on an SM");
+};
+
+// Chunk `id` (0 .. 32 chunks - 1) of a unit: keys, then values, token by token.
+template <int D>
+struct Chunk {
+    int which, t, wi;
+    __device__ __forceinline__ explicit Chunk(int id)
+        : which(id / (16 * (D / 64))), t(id % (16 * (D / 64)) / (D / 64)), wi(id % (D / 64)) {}
 };
 
 // Adds up the sequences' units and finds where warp `gw` of `warps` starts:
@@ -260,12 +272,12 @@ __device__ __forceinline__ void append_token(const uint16_t *k, const uint16_t *
 }
 
 template <int D, int G>
-__global__ void __launch_bounds__(kStoreThreads) kv4_append_kernel(const StoreArgs p) {
+__global__ void __launch_bounds__(kStoreThreads, kAppendCtas) kv4_append_kernel(const StoreArgs p) {
     using L = StoreLayout<D, G>;
     constexpr int NG = L::NG, CH = L::chunks, W8 = D / 8;
     extern __shared__ __align__(128) uint8_t smem[];
     const int lane = threadIdx.x & 31;
-    uint8_t *tile = smem + (threadIdx.x >> 5) * L::per_warp, *rec = tile + 2 * L::tile;
+    uint8_t *tile = smem + (threadIdx.x >> 5) * L::per_warp, *rec = tile + L::tile;
     for_units(p, [&](int b, const StoreWork &w, int64_t index) {
         const int i = (int)quotient(index, p.kv_heads), h = (int)(index - (int64_t)i * p.kv_heads);
         const int block = w.block0 + i;
@@ -286,34 +298,31 @@ __global__ void __launch_bounds__(kStoreThreads) kv4_append_kernel(const StoreAr
                                    p.v + (row0 + t) * p.v_stride + (int64_t)h * D, t, dst, rec, lane);
             return;
         }
-        // ---- the tokens' values, 16 bytes per lane and load ----
-        uint4 v[2][16 * W8 / 32];
+        // a pass's values, 16 bytes per lane and load
+        uint4 v[8];
+        auto load = [&](int pass) {
 #pragma unroll
-        for (int t2 = 0; t2 < 2; ++t2)
-#pragma unroll
-            for (int x = 0; x < 16 * W8 / 32; ++x) {
-                const int e = x * 32 + lane, t = e / W8;
-                v[t2][x] = t >= lo && t < end
-                               ? __ldg(reinterpret_cast<const uint4 *>(
-                                     (t2 ? p.v : p.k) + (int64_t)h * D +
-                                     (row0 + t) * (t2 ? p.v_stride : p.k_stride) + 8 * (e % W8)))
-                               : make_uint4(0u, 0u, 0u, 0u);
+            for (int x = 0; x < 8; ++x) {
+                const Chunk<D> c(32 * pass + 4 * x + lane / 8);
+                v[x] = c.t >= lo && c.t < end
+                           ? __ldg(reinterpret_cast<const uint4 *>(
+                                 (c.which ? p.v : p.k) + (int64_t)h * D +
+                                 (row0 + c.t) * (c.which ? p.v_stride : p.k_stride) + 64 * c.wi +
+                                 8 * (lane % 8)))
+                           : make_uint4(0u, 0u, 0u, 0u);
             }
-#pragma unroll
-        for (int t2 = 0; t2 < 2; ++t2)
-#pragma unroll
-            for (int x = 0; x < 16 * W8 / 32; ++x) {
-                const int e = x * 32 + lane, t = e / W8, c8 = e % W8;
-                *reinterpret_cast<uint4 *>(tile + t2 * L::tile + (t * CH + c8 / 8) * kChunkPitch +
-                                           16 * (c8 % 8)) = v[t2][x];
-            }
-        __syncwarp();
-        // ---- chunks: the keys', then the values' ----
+        };
+        load(0);
 #pragma unroll
         for (int pass = 0; pass < CH; ++pass) {
-            const int id = pass * 32 + lane, which = id / (16 * CH);
-            const int t = id % (16 * CH) / CH, wi = id % CH;
-            const uint8_t *src = tile + which * L::tile + (t * CH + wi) * kChunkPitch;
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+                *reinterpret_cast<uint4 *>(tile + (4 * x + lane / 8) * kChunkPitch + 16 * (lane % 8)) = v[x];
+            __syncwarp();
+            if (pass + 1 < CH) load(pass + 1);
+            const Chunk<D> ch(32 * pass + lane);
+            const int which = ch.which, t = ch.t, wi = ch.wi;
+            const uint8_t *src = tile + lane * kChunkPitch;
             uint4 x[8];
 #pragma unroll
             for (int q = 0; q < 8; ++q) x[q] = *reinterpret_cast<const uint4 *>(src + 16 * q);
@@ -353,9 +362,11 @@ __global__ void __launch_bounds__(kStoreThreads) kv4_append_kernel(const StoreAr
                 }
             }
             if (which == 0) {
+                // words 2 wi and 2 wi + 1 of each lane slot c are neighbours
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    *reinterpret_cast<uint32_t *>(rec + k_word_byte(D, t, 8 * wi + q)) = codes[q];
+                for (int c = 0; c < 4; ++c)
+                    *reinterpret_cast<uint2 *>(rec + k_word_byte(D, t, 8 * wi + c)) =
+                        make_uint2(codes[c], codes[4 + c]);
             } else {
                 // unit (uh, g): codes d = 16 n + 8 uh + g, n = 0..3
 #pragma unroll
@@ -373,8 +384,8 @@ __global__ void __launch_bounds__(kStoreThreads) kv4_append_kernel(const StoreAr
                     }
                 }
             }
+            __syncwarp();
         }
-        __syncwarp();
         // ---- out: the whole record, or the bytes of the call's tokens alone ----
         if (lo == 0 && end == kBlock) {
             for (int e = lane; e < L::rec / 16; e += 32)
@@ -404,42 +415,38 @@ __global__ void __launch_bounds__(kStoreThreads) kv4_append_kernel(const StoreAr
 }
 
 template <int D, int G>
-__global__ void __launch_bounds__(kStoreThreads) kv4_read_kernel(const StoreArgs p) {
+__global__ void __launch_bounds__(kStoreThreads, kReadCtas<D>) kv4_read_kernel(const StoreArgs p) {
     using L = StoreLayout<D, G>;
-    constexpr int NG = L::NG, CH = L::chunks, W8 = D / 8;
+    constexpr int NG = L::NG, CH = L::chunks, NV = L::rec / 16, VL = (NV + 31) / 32;
     extern __shared__ __align__(128) uint8_t smem[];
     const int lane = threadIdx.x & 31;
-    uint8_t *tile = smem + (threadIdx.x >> 5) * L::per_warp, *rec = tile + 2 * L::tile;
-    for_units(p, [&](int b, const StoreWork &w, int64_t index) {
-        const int i = (int)quotient(index, p.kv_heads), h = (int)(index - (int64_t)i * p.kv_heads);
-        const int block = w.block0 + i;
-        const int lo = block_lo(w, block), hi = block_hi(w, block);
-        const int64_t r = record_index(p.page_table + (int64_t)b * p.max_pages, p.max_pages,
-                                       p.num_pages, p.kv_heads, h, p.page_blocks, block);
-        const int64_t row0 = p.cu[b] + ((int64_t)block * kBlock - w.first);   // of token 0
-        if (r < 0) {
-            if (lane == 0) atomicOr(p.err_word, kErrIndex);
-        } else {
-            const uint4 *src = reinterpret_cast<const uint4 *>(p.cache + r * L::rec);
-            constexpr int NV = L::rec / 16;
-            uint4 v[(NV + 31) / 32];
+    uint8_t *tile = smem + (threadIdx.x >> 5) * L::per_warp, *rec = tile + L::tile;
+    // a unit's record is loaded while the unit before it is worked on
+    struct Unit {
+        int64_t row0;                                       // output row of token 0
+        int lo, hi, h;
+        bool ok;                                            // its page exists
+    };
+    auto give = [&](const Unit &u, const uint4 (&v)[VL]) {
+        const int64_t row0 = u.row0;
+        const int lo = u.lo, hi = u.hi, h = u.h;
 #pragma unroll
-            for (int x = 0; x < (NV + 31) / 32; ++x)
-                if (x * 32 + lane < NV) v[x] = __ldg(src + x * 32 + lane);
-#pragma unroll
-            for (int x = 0; x < (NV + 31) / 32; ++x)
-                if (x * 32 + lane < NV) reinterpret_cast<uint4 *>(rec)[x * 32 + lane] = v[x];
-        }
+        for (int x = 0; x < VL; ++x)
+            if (x * 32 + lane < NV) reinterpret_cast<uint4 *>(rec)[x * 32 + lane] = v[x];
         __syncwarp();
 #pragma unroll
         for (int pass = 0; pass < CH; ++pass) {
-            const int id = pass * 32 + lane, which = id / (16 * CH);
-            const int t = id % (16 * CH) / CH, wi = id % CH;
+            const Chunk<D> ch(32 * pass + lane);
+            const int which = ch.which, t = ch.t, wi = ch.wi;
             uint32_t codes[8];                              // word q: d = 8 q .. 8 q + 7
             if (which == 0) {
+                // words 2 wi and 2 wi + 1 of each lane slot c are neighbours
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    codes[q] = *reinterpret_cast<const uint32_t *>(rec + k_word_byte(D, t, 8 * wi + q));
+                for (int c = 0; c < 4; ++c) {
+                    const uint2 x = *reinterpret_cast<const uint2 *>(rec + k_word_byte(D, t, 8 * wi + c));
+                    codes[c] = x.x;
+                    codes[4 + c] = x.y;
+                }
             } else {
 #pragma unroll
                 for (int uh = 0; uh < 2; ++uh) {
@@ -451,7 +458,7 @@ __global__ void __launch_bounds__(kStoreThreads) kv4_read_kernel(const StoreArgs
                     units_to_nibbles(u, codes[uh], codes[2 + uh], codes[4 + uh], codes[6 + uh]);
                 }
             }
-            uint8_t *dst = tile + which * L::tile + (t * CH + wi) * kChunkPitch;
+            uint8_t *dst = tile + lane * kChunkPitch;
             constexpr int GC = G < 64 ? 64 / G : 1;         // groups of a chunk
 #pragma unroll
             for (int gc = 0; gc < GC; ++gc) {
@@ -459,7 +466,7 @@ __global__ void __launch_bounds__(kStoreThreads) kv4_read_kernel(const StoreArgs
                 uint32_t s2 = *reinterpret_cast<const uint16_t *>(
                     rec + (which ? v_scales_off(D, NG) : k_scales_off(D)) + 2 * so);
                 uint32_t z2 = rec[(which ? v_zeros_off(D, NG) : k_zeros_off(D, NG)) + so];
-                if (r < 0) s2 = z2 = 0;
+                if (!u.ok) s2 = z2 = 0;
                 s2 *= 0x00010001u;                          // (S, S)
                 z2 = (0x4300u + z2) * 0x00010001u;          // bf16(128 + Z) twice
 #pragma unroll
@@ -471,23 +478,48 @@ __global__ void __launch_bounds__(kStoreThreads) kv4_read_kernel(const StoreArgs
                     *reinterpret_cast<uint4 *>(dst + 16 * q) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
             }
-        }
-        __syncwarp();
+            __syncwarp();
 #pragma unroll
-        for (int t2 = 0; t2 < 2; ++t2) {
-            uint16_t *out = (t2 ? p.v_out : p.k_out) + (int64_t)h * D;
-#pragma unroll
-            for (int x = 0; x < 16 * W8 / 32; ++x) {
-                const int e = x * 32 + lane, t = e / W8, c8 = e % W8;
-                const int64_t row = row0 + t;
-                if (t >= lo && t < hi && row < p.T)
-                    *reinterpret_cast<uint4 *>(out + row * (int64_t)p.kv_heads * D + 8 * c8) =
-                        *reinterpret_cast<const uint4 *>(tile + t2 * L::tile +
-                                                         (t * CH + c8 / 8) * kChunkPitch + 16 * (c8 % 8));
+            for (int x = 0; x < 8; ++x) {
+                const Chunk<D> c(32 * pass + 4 * x + lane / 8);
+                const int64_t row = row0 + c.t;
+                if (c.t >= lo && c.t < hi && row < p.T)
+                    *reinterpret_cast<uint4 *>((c.which ? p.v_out : p.k_out) +
+                                               (row * p.kv_heads + h) * D + 64 * c.wi + 8 * (lane % 8)) =
+                        *reinterpret_cast<const uint4 *>(tile + (4 * x + lane / 8) * kChunkPitch +
+                                                         16 * (lane % 8));
             }
+            __syncwarp();
         }
-        __syncwarp();
+    };
+    Unit last{};
+    last.h = -1;
+    uint4 held[VL];
+    for_units(p, [&](int b, const StoreWork &w, int64_t index) {
+        const int i = (int)quotient(index, p.kv_heads), block = w.block0 + i;
+        Unit u;
+        u.h = (int)(index - (int64_t)i * p.kv_heads);
+        u.lo = block_lo(w, block);
+        u.hi = block_hi(w, block);
+        u.row0 = p.cu[b] + ((int64_t)block * kBlock - w.first);
+        const int64_t r = record_index(p.page_table + (int64_t)b * p.max_pages, p.max_pages,
+                                       p.num_pages, p.kv_heads, u.h, p.page_blocks, block);
+        u.ok = r >= 0;
+        uint4 v[VL] = {};
+        if (u.ok) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(p.cache + r * L::rec);
+#pragma unroll
+            for (int x = 0; x < VL; ++x)
+                if (x * 32 + lane < NV) v[x] = __ldg(src + x * 32 + lane);
+        } else if (lane == 0) {
+            atomicOr(p.err_word, kErrIndex);
+        }
+        if (last.h >= 0) give(last, held);
+        last = u;
+#pragma unroll
+        for (int x = 0; x < VL; ++x) held[x] = v[x];
     });
+    if (last.h >= 0) give(last, held);
 }
 
 // ---------------------------------------------------------------------------
@@ -1473,11 +1505,11 @@ qz_status dispatch(int64_t D, int64_t G, A &&...a) {
     return G == 64 ? Op<256, 64>::go(a...) : Op<256, 128>::go(a...);
 }
 
-// As many CTAs as an SM's shared memory holds, and no more than there can be
-// warps with work (a call's tokens lie in at most T / 16 + 2 B blocks).
+// One wave of CTAs, and no more than there can be warps with work (a call's
+// tokens lie in at most T / 16 + 2 B blocks).
 template <typename K>
-qz_status launch_store(K kernel, int per_warp, const StoreArgs &p, DeviceOnce &once,
-                       cudaStream_t st) {
+qz_status launch_store(K kernel, int per_warp, int ctas_per_sm, const StoreArgs &p,
+                       DeviceOnce &once, cudaStream_t st) {
     const int smem = per_warp * kStoreWarps;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) {
@@ -1493,7 +1525,7 @@ qz_status launch_store(K kernel, int per_warp, const StoreArgs &p, DeviceOnce &o
         }) != cudaSuccess)
         return QZ_ERR_CUDA;
     const int64_t most = ceil_div(((int64_t)p.T / kBlock + 2 * (int64_t)p.B) * p.kv_heads, kStoreWarps);
-    const int64_t fit = (int64_t)device_sm_count() * (220 * 1024 / (smem + 4096));
+    const int64_t fit = (int64_t)device_sm_count() * ctas_per_sm;
     kernel<<<(unsigned)(most < fit ? most : fit), kStoreThreads, smem, st>>>(p);
     return launch_status();
 }
@@ -1501,14 +1533,14 @@ template <int D, int G>
 struct Append {
     static qz_status go(const StoreArgs &p, cudaStream_t st) {
         static DeviceOnce once;
-        return launch_store(kv4_append_kernel<D, G>, StoreLayout<D, G>::per_warp, p, once, st);
+        return launch_store(kv4_append_kernel<D, G>, StoreLayout<D, G>::per_warp, kAppendCtas, p, once, st);
     }
 };
 template <int D, int G>
 struct Read {
     static qz_status go(const StoreArgs &p, cudaStream_t st) {
         static DeviceOnce once;
-        return launch_store(kv4_read_kernel<D, G>, StoreLayout<D, G>::per_warp, p, once, st);
+        return launch_store(kv4_read_kernel<D, G>, StoreLayout<D, G>::per_warp, kReadCtas<D>, p, once, st);
     }
 };
 template <int D, int G>
@@ -1576,7 +1608,7 @@ qz_status launch_kv4_attention(const Kv4Cache &c, const void *q, int64_t q_strid
     p.cu = static_cast<const int32_t *>(c.cu);
     p.T = (int)c.T; p.B = (int)c.B;
     p.max_pages = c.max_pages; p.num_pages = c.num_pages;
-    constexpr int64_t kMaxLen = (int64_t(1) << 31) - 32;
+    constexpr int64_t kMaxLen = (int64_t(1) << 31) - 128;   // positions of a step stay below 2^31
     p.capacity = (int)(c.max_pages * c.page_size < kMaxLen ? c.max_pages * c.page_size : kMaxLen);
     p.window = window < p.capacity ? (int)window : 0;      // reaches every key: none
     p.kv_heads = (int)c.kv_heads;
