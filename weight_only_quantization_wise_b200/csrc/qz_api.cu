@@ -4,7 +4,7 @@
 
 #include <atomic>
 
-#include "qz_internal.cuh"
+#include "qz_serving.cuh"
 
 namespace qz {
 

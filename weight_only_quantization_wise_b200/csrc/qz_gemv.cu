@@ -62,6 +62,7 @@
 #include <cuda_runtime.h>
 
 #include "qz_lora.cuh"
+#include "qz_serving.cuh"
 #include "qz_sm100.cuh"
 
 namespace qz {

@@ -130,25 +130,6 @@ qz_status launch_w8a16_gemv(const void *a, const void *codes, const void *scales
                             int64_t M, int64_t N, int64_t K, void *y, void *workspace,
                             const GemvPlan &plan, int overlap, cudaStream_t stream);
 
-// Low-rank adapters beside a packed projection: launch_lora (qz_lora.cu) makes
-// the first product h in `scratch` (lora_scratch_bytes), launch_gemv_lora
-// (qz_gemv.cu) is the integer GEMV that adds the second one to its sums.
-constexpr int64_t kLoraMaxRank = 128;
-struct LoraUp {
-    const uint16_t *up;        // adapters x N x rank
-    const uint16_t *h;         // [2][M][rank]: bf16 hi, lo
-    const int32_t *ids;        // adapter of each token
-    int rank, adapters;
-};
-size_t lora_scratch_bytes(int64_t M);
-qz_status launch_lora(const void *a, const void *lora_a, const void *lora_b, const void *adapters,
-                      const void *lora_scales, int64_t n_adapters, int64_t rank, int64_t M,
-                      int64_t K, void *scratch, LoraUp *up, cudaStream_t stream);
-qz_status launch_gemv_lora(int bits, const void *a, const void *codes, const void *scales,
-                           const void *zeros, int64_t M, int64_t N, int64_t K, int64_t group_size,
-                           const LoraUp &up, void *y, void *workspace, const GemvPlan &plan,
-                           cudaStream_t stream);
-
 // FP4 with block scales (qz_fp4.cu, qz_gemv.cu, qz_gemm_fp4.cu); kind 0 =
 // MXFP4, 1 = NVFP4.
 int fp4_block_size(int kind);
@@ -188,21 +169,6 @@ size_t gptq_workspace_bytes(int64_t N, int64_t K);
 qz_status launch_gptq(const void *w, const void *x, int64_t N, int64_t K, int64_t n_samples,
                       int bits, int symmetric, int64_t group_size, double damp, void *codes,
                       void *scales, void *zeros, void *workspace, cudaStream_t stream);
-
-// The paged 4-bit key/value cache (qz_kv4.cu).
-struct Kv4Cache {
-    void *cache;
-    const void *page_table, *kv_lens, *cu;     // int32 [B][max_pages], [B], [B + 1]
-    int64_t T, B, kv_heads, head_dim, group_size, page_size, num_pages, max_pages;
-};
-size_t kv4_record_bytes(int64_t head_dim, int64_t group_size);
-size_t kv4_attention_workspace_bytes(int64_t head_dim);
-qz_status launch_kv4_append(const Kv4Cache &c, const void *k, const void *v, int64_t k_stride,
-                            int64_t v_stride, cudaStream_t stream);
-qz_status launch_kv4_read(const Kv4Cache &c, void *k, void *v, cudaStream_t stream);
-qz_status launch_kv4_attention(const Kv4Cache &c, const void *q, int64_t q_stride, int64_t q_heads,
-                               float scale, int64_t window, void *out, int64_t out_stride,
-                               void *workspace, cudaStream_t stream);
 
 uint64_t device_wait_limit();
 // qz_set_launch_overlap mode (0 or 1) for the decode GEMV launches.

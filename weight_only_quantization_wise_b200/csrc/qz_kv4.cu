@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include "qz_kv4_index.cuh"
+#include "qz_serving.cuh"
 #include "qz_sm100.cuh"
 
 namespace qz {

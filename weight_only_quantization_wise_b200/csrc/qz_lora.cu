@@ -16,8 +16,8 @@
 // operands of the second product.
 #include <cuda_runtime.h>
 
-#include "qz_internal.cuh"
 #include "qz_lora.cuh"
+#include "qz_serving.cuh"
 
 namespace qz {
 namespace {
