@@ -783,7 +783,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
     }
     if (tid < 2 * WARPS) parts[tid].item_end = 0;
     if (tid == 0) abort_word = 0u;
-    if (lane < S) mbar_init(sbase + L::bars_off + 8u * (warp * S + lane), 1);
+    if (lane < S) mbar_init(sbase + L::bars_off + 8u * (warp * S + lane), 2);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     __syncthreads();
     int64_t before = 0, units = 0;
@@ -848,7 +848,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
             const int cu0 = p.cu[b];
             const int32_t *table = p.page_table + (int64_t)b * p.max_pages;
 
-            // ---- copies: step i's records go to stage (stage0 + i) % S ----
+            // ---- copies: step i's two records, lanes 0 and 1 one each ----
             // lane l holds the place of block 32 c + l of the segment, and of
             // block 32 (c + 1) + l
             const uint8_t *src_cur, *src_next;
@@ -860,23 +860,21 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
             };
             src_next = place(lane);
             uint32_t have = 0;                     // two bits per stage: its records exist
-            const int stage0 = stage;
-            auto issue = [&](int i) {
+            auto issue = [&](int i, int s) {       // step i into stage s
                 if ((i & 15) == 0) {
                     src_cur = src_next;
                     src_next = place(2 * i + 32 + lane);
                 }
                 const uint8_t *src = reinterpret_cast<const uint8_t *>(__shfl_sync(
-                    0xFFFFFFFFu, reinterpret_cast<unsigned long long>(src_cur), ((2 * i) & 31) + (lane & 1)));
+                    0xFFFFFFFFu, reinterpret_cast<unsigned long long>(src_cur), 2 * i + (lane & 1)));
                 const uint32_t got = __ballot_sync(0xFFFFFFFFu, src != nullptr) & 3u;
-                int s = stage0 + i % S;
-                if (s >= S) s -= S;
                 have = (have & ~(3u << (2 * s))) | got << (2 * s);
-                const uint32_t bar = bar0 + 8u * s;
-                if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)L::rec * __popc(got));
-                __syncwarp();
-                if (lane < 2 && src != nullptr)
-                    bulk_copy(ring + (uint32_t)(2 * s + lane) * L::rec, src, (uint32_t)L::rec, bar);
+                if (lane < 2) {
+                    const uint32_t bar = bar0 + 8u * s;
+                    mbar_arrive_expect_tx(bar, src != nullptr ? (uint32_t)L::rec : 0u);
+                    if (src != nullptr)
+                        bulk_copy(ring + (uint32_t)(2 * s + lane) * L::rec, src, (uint32_t)L::rec, bar);
+                }
             };
             // ---- queries: row gid of each 8-row tile ----
             uint4 qx[NB][KW];
@@ -895,7 +893,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                     qx[nb][j] = src ? __ldg(reinterpret_cast<const uint4 *>(src + 32 * j))
                                     : make_uint4(0u, 0u, 0u, 0u);
             }
-            for (int i = 0; i < S && i < steps; ++i) issue(i);
+            for (int i = 0; i < S && i < steps; ++i) issue(i, stage + i < S ? stage + i : stage + i - S);
 
             // ---- queries as B fragments ----
             uint32_t qf[L::q_smem ? 1 : NB][L::q_smem ? 1 : 4 * KW];
@@ -1252,8 +1250,8 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                 // every register loaded from the stage has been consumed by an
                 // MMA or a conversion: it may be filled again
                 __syncwarp();
+                if (i + S < steps) issue(i + S, stage);
                 if (++stage == S) { stage = 0; phase ^= 1u; }
-                if (i + S < steps) issue(i + S);
             }
             if (!ok) break;
 
