@@ -200,6 +200,11 @@ def test_python_argument_checks(dev):
                 dict(lora_scales=ls.cpu()), dict(lora_b=up.transpose(0, 1).contiguous())):
         with pytest.raises(ValueError):
             qz.qz_w4a16_lora_gemv(a, c, s, z, N, K, **dict(good, **bad))
+    for bad in ((c[:, :32], s, z), (c, s.float(), z), (c, s, z[:1]), (c.cpu(), s, z)):
+        with pytest.raises(ValueError):
+            qz.qz_w4a16_lora_gemv(a, *bad, N, K, down, up, ids, ls)
+    with pytest.raises(ValueError):
+        qz.qz_w4a16_lora_gemv(a, c, s, z, N, K, down, up, ids, ls, y=torch.empty_like(a))
     with pytest.raises(qz.QzError):                  # rank not a multiple of 8
         qz.qz_w4a16_lora_gemv(a, c, s, z, N, K, down[:, :12].contiguous(),
                               up[:, :, :12].contiguous(), ids, ls)

@@ -493,12 +493,11 @@ def _lora_args(a, N, K, lora_a, lora_b, adapters, lora_scales):
             rank)
 
 
-def _lora_out(a, N, y):
-    if y is None:
-        return torch.empty((a.shape[0], N), dtype=torch.bfloat16, device=a.device)
-    if y.dtype is not torch.bfloat16 or tuple(y.shape) != (a.shape[0], N) or y.device != a.device:
-        raise ValueError("y must be an (M, N) bf16 tensor on a's device")
-    return y
+def _array(t, name, dtype, n, dev):
+    """Address of a contiguous tensor of n values on `dev`."""
+    if t.dtype is not dtype or t.numel() != n or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} values on a's device")
+    return t.data_ptr()
 
 
 def qz_w4a16_lora_gemv(a, codes, scales, zeros, N, K, lora_a, lora_b, adapters, lora_scales,
@@ -510,13 +509,18 @@ def qz_w4a16_lora_gemv(a, codes, scales, zeros, N, K, lora_a, lora_b, adapters, 
     la, lb, ids, ls, n, rank = _lora_args(a, N, K, lora_a, lora_b, adapters, lora_scales)
     M = a.shape[0]
     with _scope(dev, stream):
-        y = _lora_out(a, N, y)
+        if y is None:
+            y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        yp = _array(y, "y", torch.bfloat16, M * N, dev)
         nbytes = qz_workspace_bytes(QZ_OP_W4A16_LORA_GEMV, M, N, K, group_size)
+        cp = _array(codes, "codes", torch.uint8, N * K // 2, dev)
+        sp = _array(scales, "scales", torch.bfloat16, N * (K // group_size), dev)
+        zp = _array(zeros, "zeros", torch.uint8, N * (K // group_size), dev)
         ws_ptr, ws_bytes = _ws_args(workspace, nbytes, dev, _matmul_key(
             QZ_OP_W4A16_LORA_GEMV, M, N, K, group_size, scales, zeros))
-        _check(lib.qz_w4a16_lora_gemv(a.data_ptr(), _ptr(codes), _ptr(scales), _ptr(zeros), M, N, K,
-                                      group_size, la, lb, ids, ls, n, rank, _ptr(y), ws_ptr,
-                                      ws_bytes, _stream_of(dev, stream)), "qz_w4a16_lora_gemv")
+        _check(lib.qz_w4a16_lora_gemv(a.data_ptr(), cp, sp, zp, M, N, K, group_size, la, lb, ids, ls,
+                                      n, rank, yp, ws_ptr, ws_bytes, _stream_of(dev, stream)),
+               "qz_w4a16_lora_gemv")
     return y
 
 
@@ -527,12 +531,16 @@ def qz_w8a16_lora_gemv(a, codes, scales, N, K, lora_a, lora_b, adapters, lora_sc
     la, lb, ids, ls, n, rank = _lora_args(a, N, K, lora_a, lora_b, adapters, lora_scales)
     M = a.shape[0]
     with _scope(dev, stream):
-        y = _lora_out(a, N, y)
+        if y is None:
+            y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        yp = _array(y, "y", torch.bfloat16, M * N, dev)
         nbytes = qz_workspace_bytes(QZ_OP_W8A16_LORA_GEMV, M, N, K, K)
+        cp = _array(codes, "codes", torch.uint8, N * K, dev)
+        sp = _array(scales, "scales", torch.bfloat16, N, dev)
         ws_ptr, ws_bytes = _ws_args(workspace, nbytes, dev, (QZ_OP_W8A16_LORA_GEMV, M, N, K))
-        _check(lib.qz_w8a16_lora_gemv(a.data_ptr(), _ptr(codes), _ptr(scales), M, N, K, la, lb, ids,
-                                      ls, n, rank, _ptr(y), ws_ptr, ws_bytes,
-                                      _stream_of(dev, stream)), "qz_w8a16_lora_gemv")
+        _check(lib.qz_w8a16_lora_gemv(a.data_ptr(), cp, sp, M, N, K, la, lb, ids, ls, n, rank, yp,
+                                      ws_ptr, ws_bytes, _stream_of(dev, stream)),
+               "qz_w8a16_lora_gemv")
     return y
 
 

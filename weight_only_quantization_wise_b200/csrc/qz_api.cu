@@ -95,14 +95,6 @@ qz_status check_fp4a4(int64_t M, int64_t N, int64_t K, int32_t kind) {
     return QZ_OK;
 }
 
-// The GEMV's part of a LoRA GEMV's workspace (a multiple of 256 bytes; the
-// adapters' scratch lies behind it).
-size_t lora_gemv_bytes(int bits, int64_t M, int64_t N, int64_t K, int64_t group_size) {
-    const size_t b = bits == 4 ? gemv_workspace_bound(M, N, K, 4, gemv_unit_k(4, M, N, K, group_size))
-                               : gemv_workspace_bound(M, N, K, 8);
-    return (b + 255) & ~(size_t)255;
-}
-
 }  // namespace
 }  // namespace qz
 
@@ -192,8 +184,11 @@ QZ_API qz_status qz_workspace_bytes(int32_t op, int64_t M, int64_t N, int64_t K,
     case QZ_OP_W8A16_LORA_GEMV: {
         const qz_status s = check_gemv_shape(M, N, K);
         if (s != QZ_OK) return s;
-        *bytes = lora_gemv_bytes(op == QZ_OP_W4A16_LORA_GEMV ? 4 : 8, M, N, K, group_size) +
-                 lora_scratch_bytes(M);
+        // the adapters' scratch, then the plain GEMV's workspace
+        *bytes = lora_scratch_bytes(M) +
+                 (op == QZ_OP_W4A16_LORA_GEMV
+                      ? gemv_workspace_bound(M, N, K, 4, gemv_unit_k(4, M, N, K, group_size))
+                      : gemv_workspace_bound(M, N, K, 8));
         return QZ_OK;
     }
     case QZ_OP_KV4_ATTENTION:
@@ -487,21 +482,21 @@ qz_status lora_gemv(int bits, const void *a, const void *codes, const void *scal
     if (!aligned(lora_a, 16) || !aligned(lora_b, 16) || !aligned(adapters, 4) ||
         !aligned(lora_scales, 4))
         return QZ_ERR_ALIGNMENT;
-    const size_t base = lora_gemv_bytes(bits, M, N, K, group_size);
-    qz_status s = check_workspace(base + lora_scratch_bytes(M), workspace, workspace_bytes);
-    if (s != QZ_OK) return s;
     const GemvPlan plan =
         bits == 4 ? gemv_plan(M, N, K, 4, device_sm_count(),
                               gemv_unit_k(4, M, N, K, group_size, scales, zeros))
                   : gemv_plan(M, N, K, 8, device_sm_count());
+    const size_t scratch = lora_scratch_bytes(M);          // a multiple of 256
+    qz_status s = check_workspace(scratch + plan.total_bytes, workspace, workspace_bytes);
+    if (s != QZ_OK) return s;
     LoraUp up;
-    s = launch_lora(a, lora_a, lora_b, adapters, lora_scales, n_adapters, rank, M, K,
-                    static_cast<char *>(workspace) + base, &up, st);
+    s = launch_lora(a, lora_a, lora_b, adapters, lora_scales, n_adapters, rank, M, K, workspace, &up,
+                    st);
     if (s != QZ_OK) return s;
     // The GEMV overlaps the kernel that makes h, which writes nothing else that
     // it reads and starts only after whatever was queued before this call.
-    return launch_gemv_lora(bits, a, codes, scales, zeros, M, N, K, group_size, up, y, workspace,
-                            plan, st);
+    return launch_gemv_lora(bits, a, codes, scales, zeros, M, N, K, group_size, up, y,
+                            static_cast<char *>(workspace) + scratch, plan, st);
 }
 
 }  // namespace
