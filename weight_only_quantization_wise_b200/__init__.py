@@ -508,6 +508,8 @@ def qz_w4a16_lora_gemv(a, codes, scales, zeros, N, K, lora_a, lora_b, adapters, 
     dev = a.device
     la, lb, ids, ls, n, rank = _lora_args(a, N, K, lora_a, lora_b, adapters, lora_scales)
     M = a.shape[0]
+    if group_size < 1:
+        raise ValueError("group_size must be positive")
     with _scope(dev, stream):
         if y is None:
             y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
