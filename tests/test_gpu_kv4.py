@@ -205,6 +205,17 @@ def test_attention_several_tokens(dev, D, g, new, window):
     check_attention(dev, D, g, 32, 2, 3, [80, 41, 33], new, window=window, seed=7)
 
 
+@pytest.mark.parametrize("D,g", ref.COMBOS)
+@pytest.mark.parametrize("lens,new,extra", [([300, 41, 90], [50, 13, 1], 0), ([300, 41, 90], [50, 12, 1], 0),
+                                            ([3000], [67], 0), ([40, 0, 7], [60, 0, 2], 9)])
+@pytest.mark.parametrize("window", [0, 20])
+def test_attention_of_prompt_parts(dev, D, g, lens, new, extra, window):
+    """Many rows per key head (64 tokens of 8 heads make 128 tiles of 8 rows,
+    from where tiles of 16 are used; 63 do not), tiles cut by the sequences'
+    ends, rows in front of the first key, rows of no sequence."""
+    check_attention(dev, D, g, 32, 2, 8, lens, new, window=window, T_extra=extra, seed=14)
+
+
 def test_attention_rows_without_keys(dev):
     """No cached tokens, and more query rows than cached tokens: the rows in
     front of the first key give zeros."""

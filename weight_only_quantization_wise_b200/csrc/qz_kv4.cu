@@ -598,21 +598,18 @@ constexpr int attn_smem(int ctas) { return (ctas == 2 ? 108 : 221) * 1024; }
 template <int D, int G, int NB, int WARPS, int CTAS>
 struct AttnLayout {
     static constexpr int NG = D / G;
-    static constexpr bool q_smem = D == 256 && NB == 2;    // queries do not fit in registers
     static constexpr int rec = (int)record_bytes(D, G);
     static constexpr int slot = Slot<D, NB>::bytes;
-    static constexpr int q_bytes = q_smem ? 8 * NB * D * 2 : 0;
     static constexpr int ring_bytes(int s) {
         return ((2 * s * rec > slot ? 2 * s * rec : slot) + 15) & ~15;
     }
-    static constexpr int total(int s) { return WARPS * (ring_bytes(s) + slot + q_bytes + 8 * s); }
+    static constexpr int total(int s) { return WARPS * (ring_bytes(s) + slot + 8 * s); }
     // stages (two records each) in flight per warp
     static constexpr int S = total(3) <= attn_smem(CTAS) ? 3 : 2;
     static constexpr int ring = ring_bytes(S);
     static constexpr int ring_off = 0;                     // [WARPS][ring]; later part 1 of a warp
     static constexpr int first_off = WARPS * ring;         // [WARPS][slot]: part 0
-    static constexpr int q_off = first_off + WARPS * slot;
-    static constexpr int bars_off = q_off + WARPS * q_bytes;
+    static constexpr int bars_off = first_off + WARPS * slot;
     static constexpr int bytes = bars_off + WARPS * S * 8;
     static_assert(bytes <= attn_smem(CTAS), "the CTAs fit on an SM");
     static_assert(rec % 16 == 0 && slot % 16 == 0, "bulk copies and slots are 16-byte aligned");
@@ -896,8 +893,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
             for (int i = 0; i < S && i < steps; ++i) issue(i, stage + i < S ? stage + i : stage + i - S);
 
             // ---- queries as B fragments ----
-            uint32_t qf[L::q_smem ? 1 : NB][L::q_smem ? 1 : 4 * KW];
-            const uint32_t q_area = sbase + L::q_off + (uint32_t)warp * L::q_bytes + 16u * lane;
+            uint32_t qf[NB][4 * KW];
             float kq[NB][2];                       // per column 2 tig, 2 tig + 1
             int qsum[NG][NB][2];                   // sum_d i_d of each group
 #pragma unroll
@@ -939,14 +935,8 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                         f4[odd] = dev::prmt(a, c, 0x7632u);        // high bytes
                         f4[2 + odd] = dev::prmt(a, c, 0x5410u);    // low bytes
                     }
-                    if constexpr (L::q_smem) {
-                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
-                                         q_area + 512u * (uint32_t)(j * NB + nb)),
-                                     "r"(f4[0]), "r"(f4[1]), "r"(f4[2]), "r"(f4[3]) : "memory");
-                    } else {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) qf[nb][4 * j + i] = f4[i];
-                    }
+                    for (int i = 0; i < 4; ++i) qf[nb][4 * j + i] = f4[i];
                 }
                 // a row with an infinity or a NaN gives NaN
                 const float kr = big >= 0x7F80u ? __int_as_float(0x7FFFFFFF)
@@ -1021,17 +1011,6 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
 #pragma unroll
                         for (int jj = 0; jj < G / 32; ++jj) {
                             const int j = gr * (G / 32) + jj;
-                            uint4 qv[NB];
-#pragma unroll
-                            for (int nb = 0; nb < NB; ++nb) {
-                                if constexpr (L::q_smem)
-                                    qv[nb] = *reinterpret_cast<const uint4 *>(
-                                        smem + L::q_off + warp * L::q_bytes + 16 * lane +
-                                        512 * (j * NB + nb));
-                                else
-                                    qv[nb] = make_uint4(qf[nb][4 * j], qf[nb][4 * j + 1],
-                                                        qf[nb][4 * j + 2], qf[nb][4 * j + 3]);
-                            }
 #pragma unroll
                             for (int rc = 0; rc < 2; ++rc) {
                                 const uint32_t a = kw[rc][0][j], c = kw[rc][1][j];
@@ -1040,11 +1019,11 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
 #pragma unroll
                                 for (int nb = 0; nb < NB; ++nb) {
                                     if (jj == 0) {
-                                        mma_i8<false, true>(th[rc][nb], a0, a1, a2, a3, qv[nb].x, qv[nb].y);
-                                        mma_i8<false, false>(tl[rc][nb], a0, a1, a2, a3, qv[nb].z, qv[nb].w);
+                                        mma_i8<false, true>(th[rc][nb], a0, a1, a2, a3, qf[nb][4 * j], qf[nb][4 * j + 1]);
+                                        mma_i8<false, false>(tl[rc][nb], a0, a1, a2, a3, qf[nb][4 * j + 2], qf[nb][4 * j + 3]);
                                     } else {
-                                        mma_i8<true, true>(th[rc][nb], a0, a1, a2, a3, qv[nb].x, qv[nb].y);
-                                        mma_i8<true, false>(tl[rc][nb], a0, a1, a2, a3, qv[nb].z, qv[nb].w);
+                                        mma_i8<true, true>(th[rc][nb], a0, a1, a2, a3, qf[nb][4 * j], qf[nb][4 * j + 1]);
+                                        mma_i8<true, false>(tl[rc][nb], a0, a1, a2, a3, qf[nb][4 * j + 2], qf[nb][4 * j + 3]);
                                     }
                                 }
                             }
@@ -1458,14 +1437,29 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
 // 8-row tiles stay in registers (and the rings of 4 groups in shared memory).
 constexpr int kAttnCtasPerSm = 2;      // at most
 template <int D, int NB>
-constexpr int kAttnCtas = (D == 128 && NB == 1) || (D == 256 && NB == 2) ? 1 : kAttnCtasPerSm;
+constexpr int kAttnCtas = D == 128 && NB == 1 ? 1 : kAttnCtasPerSm;
 template <int D, int G, int NB>
 constexpr int kAttnWarps =
-    D == 256 ? (NB == 1 ? 4 : 5) : NB == 2 ? 6 : D == 64 ? 8 : G == 32 ? 14 : 16;
+    D == 256 ? 4 : NB == 2 ? 6 : D == 64 ? 8 : G == 32 ? 14 : 16;
 
-// Rows of a tile: 8 when a sequence has at most 8 rows per key head on
-// average, else 16 (the keys are read once per tile).
-int attn_tiles(int64_t T, int64_t B, int64_t share) { return T * share <= 8 * B ? 1 : 2; }
+// Rows of a tile: 8 or 16.  A tile of 16 reads and unpacks the keys once for
+// twice the rows, but has half the warps per CTA and twice the products and
+// softmax per step.  Warm, 8 key heads, 8- against 16-row tiles:
+//   D = 64, one scale per head:   64 x 4000 tokens, 16 rows per key head 84, 68 us;
+//       512 rows 2165, 1606; 1 x 32000, 16 rows 23, 31; 128 rows 81, 67
+//   D = 128, g = 32:   64 x 4000, 16 rows 187, 175; 512 rows 5315, 4526
+//   D = 128, g = 64:   16 rows 134, 146; 512 rows 3590, 3740
+//   D = 128, g = 128:  16 rows 116, 124; 512 rows 3321, 3105; 1 x 32000, 16 rows 30, 46
+//   D = 256, g = 128:  16 rows 196, 250; 128 rows 1550, 1856
+// So 16 for 64-wide heads and for groups of 32, when a sequence has more than 8
+// rows on average and the 8-row tiles come to 128 or more (below that the longer
+// tiles leave the machine idle).
+template <int D, int G>
+constexpr bool kTallTiles = D == 64 || G == 32;
+bool tall_tiles(const AttnArgs &p) {
+    const int64_t rows = (int64_t)p.T * p.share;
+    return rows > 8 * (int64_t)p.B && rows * p.kv_heads >= 8 * 128;
+}
 
 template <int D, int G, int NB>
 qz_status launch_attn(const AttnArgs &in, cudaStream_t st) {
@@ -1544,8 +1538,10 @@ struct Read {
 };
 template <int D, int G>
 struct Attend {
-    static qz_status go(const AttnArgs &p, int tiles, cudaStream_t st) {
-        return tiles == 1 ? launch_attn<D, G, 1>(p, st) : launch_attn<D, G, 2>(p, st);
+    static qz_status go(const AttnArgs &p, cudaStream_t st) {
+        if constexpr (kTallTiles<D, G>)
+            if (tall_tiles(p)) return launch_attn<D, G, 2>(p, st);
+        return launch_attn<D, G, 1>(p, st);
     }
 };
 
@@ -1616,14 +1612,13 @@ qz_status launch_kv4_attention(const Kv4Cache &c, const void *q, int64_t q_strid
     p.scale_log2 = (float)((double)scale * 1.4426950408889634);
     p.out = static_cast<uint16_t *>(out);
     p.out_stride = out_stride;
-    const int tiles = attn_tiles(c.T, c.B, p.share);
     // counters first: their place does not depend on the tile size
     p.counters = static_cast<uint32_t *>(workspace);
     p.partials = reinterpret_cast<float *>(static_cast<char *>(workspace) + kCounterBytes);
     p.wait_limit = device_wait_limit();
     p.err_word = device_error_word();
     if (p.err_word == nullptr) return QZ_ERR_CUDA;
-    return dispatch<Attend>(c.head_dim, c.group_size, p, tiles, st);
+    return dispatch<Attend>(c.head_dim, c.group_size, p, st);
 }
 
 }  // namespace qz
