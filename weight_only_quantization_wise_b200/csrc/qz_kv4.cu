@@ -27,7 +27,14 @@ constexpr unsigned kErrIndex = 2u;     // bit of the device error word: bad page
 // one token ("chunk"), which hold whole groups (or half a group of 128) and
 // whole 32-bit words of K and 16-bit units of V; a pass is 32 chunks.  Passes'
 // values and the record go through the warp's shared memory, so that global
-// memory is read and written in whole rows and whole records.
+// memory is read and written in whole rows and whole records.  (With a warp per
+// token and head and scattered stores, 8057 prompt tokens written and read back
+// took 76 us instead of 35, cold; 8 key heads of 128.)
+// Measured there, warm: append 14.0 us, read 10.0 us (42 MB each: 0.47 and 0.65
+// of the 6449 GB/s of a copy); 35 thousand tokens read back cold 41 us (175 MB,
+// 0.66), 45 us without the next unit's record under way.  The read issues on
+// 0.37 of the cycles and waits mostly for loads (counters, before that
+// prefetch): latency, not instructions.  The append was not profiled.
 struct StoreArgs {
     const uint16_t *k, *v;             // append: input
     uint16_t *k_out, *v_out;           // read: output
@@ -292,6 +299,8 @@ __global__ void __launch_bounds__(kStoreThreads, kAppendCtas) kv4_append_kernel(
         const int64_t row0 = p.cu[b] + ((int64_t)block * kBlock - w.first);   // of token 0
         uint8_t *dst = p.cache + r * L::rec;
         const int end = (int)min((int64_t)hi, p.T - row0);
+        // few tokens, as in decoding: one at a time, all lanes on it (one new
+        // token of each of 32 sequences 3.9 us, by the passes below 6.4)
         if (end - lo <= 2) {
             // ---- a token or two (decoding): a lane takes D / 32 values ----
             for (int t = lo; t < end; ++t)
@@ -561,6 +570,19 @@ __global__ void __launch_bounds__(kStoreThreads, kReadCtas<D>) kv4_read_kernel(c
 // result, so that the probabilities only need an 8 x 8 transpose between the
 // two).  An item cut by warps is joined in shared memory, one cut by CTAs in
 // the workspace by the last to arrive, parts added in order.
+//
+// Measured, 8 key heads of 128: 128 sequences of 1000..16000 tokens (785 MB, 32
+// query heads) 161 us warm, 176 cold: 0.69 of the copy bandwidth, at the power
+// limit (995 W, 1820 MHz).  A record of 16 tokens costs 271 warp instructions,
+// 113 of them integer and logic, 97 on the multiply pipes, 17 loads; they bind
+// before the bytes do.  Shorter calls are bound by launch, prologue and joins:
+// one sequence of 131001 tokens (64 query heads, two scales per head, 147 MB) 51
+// us warm, one of 777 tokens 12 us.
+// Tried: three stages a ring instead of two (batch 167 against 170 us warm, 184
+// against 180 cold: not a matter of latency); two CTAs of 6 warps instead of 8
+// (201, 200); fp16 products for the scores (197 us cold against 180).  Without
+// the subtraction of Z from the codes of V (a timing probe) the batch took 11%
+// less, but the subnormal codes that would allow it lose low bits in the product.
 struct AttnArgs {
     const uint16_t *q;
     int64_t q_stride;                  // elements between tokens
@@ -1435,6 +1457,9 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
 // ---------------------------------------------------------------------------
 // CTAs per SM, and warps per CTA so that the accumulators and queries of NB
 // 8-row tiles stay in registers (and the rings of 4 groups in shared memory).
+// D = 128, warm: one CTA of 16 warps against two of 8, half the parts to join:
+// one long sequence 51, 58 us, batch 166, 171.  D = 64 has many short items and
+// takes two: 17 sequences of draft tokens 27 us, with one CTA 32.
 constexpr int kAttnCtasPerSm = 2;      // at most
 template <int D, int NB>
 constexpr int kAttnCtas = D == 128 && NB == 1 ? 1 : kAttnCtasPerSm;
@@ -1480,11 +1505,14 @@ qz_status launch_attn(const AttnArgs &in, cudaStream_t st) {
             return e;
         }) != cudaSuccess)
         return QZ_ERR_CUDA;
-    // two steps of two blocks per warp at least: with less, a CTA's prologue and
-    // join outweigh its loop (8 warps: 16 and 32 units measured alike, 64 slower)
+    // two steps of two blocks per warp at least, as a CTA's prologue and join
+    // outweigh a shorter loop.  Mixed batch of 12, D = 256, 16-row tiles, warm: 2,
+    // 4, 8 units per warp 35, 35, 42 us; other calls alike.
     AttnArgs args = in;
     args.min_units = 4 * W;
-    args.whole_units = 12 * W;                     // a CTA's six steps per warp
+    // items alike of up to six steps per warp whole in a CTA, not cut: one
+    // sequence of 777 tokens 11.7 us, cut 18.5; other calls alike
+    args.whole_units = 12 * W;
     kernel<<<(unsigned)(device_sm_count() * C), 32 * W, L::bytes, st>>>(args);
     return launch_status();
 }
