@@ -136,6 +136,23 @@ def test_unused_adapters_are_not_read_and_wild_indices_are_reported(dev):
     assert (err <= bound(want, mag, lmag)).all()
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("M", [4, 12, 40])
+@pytest.mark.parametrize("where", ["down", "up", "scale"])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_an_adapter_that_is_not_finite_harms_its_own_tokens_alone(dev, bits, M, where, value):
+    N, K, R = 200, 512, 24
+    w, a = synthetic.weights(N, K, seed=6), synthetic.activations(M, K, seed=6)
+    down, up, ls = adapter_set(3, N, K, R, 4)
+    ids = [m % 4 - 1 for m in range(M)]
+    clean = run(dev, bits, w, a, down, up, ids, ls, 128)
+    {"down": down, "up": up, "scale": ls}[where][1] = value
+    got = run(dev, bits, w, a, down, up, ids, ls, 128)
+    others = [m for m in range(M) if ids[m] != 1]
+    assert torch.equal(got[others], clean[others])
+    assert not got[[m for m in range(M) if ids[m] == 1]].isfinite().any()
+
+
 def test_adapter_gradients_of_scale(dev):
     """y is affine in lora_scales: the difference of two calls is the adapter's
     part alone, to the rounding of the outputs."""

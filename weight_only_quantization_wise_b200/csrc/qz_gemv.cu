@@ -654,8 +654,9 @@ __device__ __forceinline__ void lora_warm(const GemvArgs &p, int lane) {
     }
 }
 // acc (layout as for gemv_flush) += the part of one adapter (tokens `tokens`;
-// columns of other tokens are zero) for the warp's 32 rows of B at `rows`.  A
-// lane reads 16 bytes of a row: ranks 8 t .. 8 t + 7 of every 32.
+// columns of other tokens are left out: an adapter that is not finite would
+// reach them through 0 * inf) for the warp's 32 rows of B at `rows`.  A lane
+// reads 16 bytes of a row: ranks 8 t .. 8 t + 7 of every 32.
 template <int MB>
 __device__ __forceinline__ void lora_add(float (&acc)[2][MB][4], const GemvArgs &p, uint32_t rows,
                                          uint64_t tokens, int lane) {
@@ -705,8 +706,9 @@ __device__ __forceinline__ void lora_add(float (&acc)[2][MB][4], const GemvArgs 
             for (int rt = 0; rt < 2; ++rt)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    acc[rt][mb][i] += (sum[0][0][rt][i] + sum[1][0][rt][i]) +
-                                      (sum[0][1][rt][i] + sum[1][1][rt][i]);
+                    if ((tokens >> (8 * mb + 2 * t + (i & 1))) & 1ull)
+                        acc[rt][mb][i] += (sum[0][0][rt][i] + sum[1][0][rt][i]) +
+                                          (sum[0][1][rt][i] + sum[1][1][rt][i]);
         }
     }
 }
