@@ -481,3 +481,35 @@ def test_infinite_and_nan_queries(dev):
     assert got[0, 2].isnan().all() and got[0, 4].isnan().all()
     keep = [0, 1, 3, 5, 6, 7]
     assert torch.equal(got[0, keep], clean[0, keep])
+
+
+def attend_values(dev, k, v, q, new, g, window=0):
+    """Attention over one sequence, and the 64-bit form over its finite tokens
+    (what stands at the others must not be seen by the rows compared)."""
+    L, H, D = k.shape
+    c = Cache(dev, [L], H, D, 16, g)
+    c.append(k.to(dev), v.to(dev), [L], [L])
+    got = c.attend(q.to(dev), [L], [new], window=window).cpu().double().numpy()
+    fine = [torch.where(x.isfinite().all(-1, keepdim=True), x, torch.zeros_like(x)) for x in (k, v)]
+    kq, vq = ref.quantize(fine[0], g), ref.quantize(fine[1], g)
+    kv = [(ref.values(*kq, g), ref.values(*vq, g), ref.bf16_f64(kq[1]).max(-1),
+           ref.bf16_f64(vq[1]).max(-1))]
+    want, parts = ref.attention(q.double().numpy(), kv, [L], [new], D ** -0.5, window)
+    return got, want, ref.bound(want, parts, D)
+
+
+@pytest.mark.parametrize("D,g", ref.COMBOS)
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_keys_a_row_may_not_see_change_nothing(dev, D, g, value, which):
+    """The last token holds a value that only the last query may see, the first
+    one a value that the window hides from all."""
+    L, new = 40, 3
+    k, v = keys((L, 1, D), 21), randn((L, 1, D), 22)
+    x = k if which == "k" else v
+    x[L - 1, 0, 5] = value
+    x[0, 0, 7] = value
+    got, want, lim = attend_values(dev, k, v, randn((new, 2, D), 23), new, g, window=30)
+    assert (np.abs(got - want)[:new - 1] <= lim[:new - 1]).all()
+    if value == float("inf"):              # a NaN is left out by quantize_pack: its scale is finite
+        assert not np.isfinite(got[new - 1]).all()

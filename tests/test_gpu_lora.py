@@ -153,6 +153,18 @@ def test_an_adapter_that_is_not_finite_harms_its_own_tokens_alone(dev, bits, M, 
     assert not got[[m for m in range(M) if ids[m] == 1]].isfinite().any()
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+def test_a_low_rank_product_past_bf16_is_infinite(dev, bits):
+    """512 products of 1e37 pass the largest number: the output's sign is B's."""
+    N, K, M = 128, 512, 2
+    w, a = synthetic.weights(N, K, seed=7), torch.ones(M, K, dtype=torch.bfloat16)
+    down, up = torch.full((1, 8, K), 1e37), torch.ones(1, N, 8)
+    up[0, N // 2:] = -1.0
+    y = run(dev, bits, w, a, down.to(torch.bfloat16), up.to(torch.bfloat16), [0] * M,
+            torch.ones(1), 128)
+    assert (y[:, :N // 2] == float("inf")).all() and (y[:, N // 2:] == float("-inf")).all()
+
+
 def test_adapter_gradients_of_scale(dev):
     """y is affine in lora_scales: the difference of two calls is the adapter's
     part alone, to the rounding of the outputs."""

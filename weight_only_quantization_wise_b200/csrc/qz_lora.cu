@@ -136,9 +136,11 @@ lora_down_kernel(const LoraArgs p) {
             const int j = j0 + threadIdx.x / 16, t = nth_token(mask, threadIdx.x % 16);
             if (t >= 0 && j < p.R) {
                 const uint32_t hi = dev::f32_to_bf16_rne(h);
+                const float top = __uint_as_float(hi << 16);
                 p.h[(int64_t)t * p.R + j] = (uint16_t)hi;
+                // beside an infinity (or a NaN) nothing: inf - inf is not its rest
                 p.h[(int64_t)(p.M + t) * p.R + j] =
-                    (uint16_t)dev::f32_to_bf16_rne(h - __uint_as_float(hi << 16));
+                    isfinite(top) ? (uint16_t)dev::f32_to_bf16_rne(h - top) : (uint16_t)0;
             }
         }
         cluster_sync();                                      // sums have been read
