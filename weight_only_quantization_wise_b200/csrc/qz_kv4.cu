@@ -1104,7 +1104,13 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                             for (int x = 0; x < 2; ++x) {
                                 const int key = key0 + 16 * rc + gid + 8 * x;
                                 const bool none = !((got >> rc) & 1u) || key >= sw.len;
-                                if (none) {                     // not written: whatever it holds
+                                // a scale that is not finite (values that were not) makes
+                                // the rows that see the key NaN, and may not reach the
+                                // others through 0 * inf
+                                bool wild = false;
+#pragma unroll
+                                for (int gr = 0; gr < NG; ++gr) wild |= !(vs[rc][gr][x] <= 3.4e38f);
+                                if (none || wild) {             // none: not written, whatever it holds
 #pragma unroll
                                     for (int gr = 0; gr < NG; ++gr) vs[rc][gr][x] = 0.0f;
                                 }
@@ -1114,6 +1120,8 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                                     for (int c = 0; c < 2; ++c)
                                         if (none || key >= khi[nb][c] || key < klo[nb][c])
                                             s[rc][nb][2 * x + c] = __int_as_float(0xFF800000);
+                                        else if (wild)
+                                            s[rc][nb][2 * x + c] = __int_as_float(0x7FFFFFFF);
                             }
                     }
                     // -- 2^(s - m) (times the scale when there is one per key): s is
