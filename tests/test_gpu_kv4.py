@@ -499,7 +499,7 @@ def attend_values(dev, k, v, q, new, g, window=0):
 
 
 @pytest.mark.parametrize("D,g", ref.COMBOS)
-@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+@pytest.mark.parametrize("value", [float("inf"), float("nan"), 1e25])
 @pytest.mark.parametrize("which", ["k", "v"])
 def test_keys_a_row_may_not_see_change_nothing(dev, D, g, value, which):
     """The last token holds a value that only the last query may see, the first
@@ -513,3 +513,34 @@ def test_keys_a_row_may_not_see_change_nothing(dev, D, g, value, which):
     assert (np.abs(got - want)[:new - 1] <= lim[:new - 1]).all()
     if value == float("inf"):              # a NaN is left out by quantize_pack: its scale is finite
         assert not np.isfinite(got[new - 1]).all()
+
+
+@pytest.mark.parametrize("D,g", ref.COMBOS)
+@pytest.mark.parametrize("power", [-40, -20, 20, 40])
+def test_rows_of_values_of_different_sizes(dev, D, g, power):
+    """Heads of one tile that look at keys whose values differ in size by far."""
+    L = 40
+    k, v = torch.zeros(L, 1, D), randn((L, 1, D), 31).float()
+    k[3, 0, :D // 2], k[35, 0, D // 2:] = 4.0, 4.0
+    v[35] *= 2.0 ** power
+    q = torch.zeros(1, 2, D)
+    q[0, 0, :D // 2], q[0, 1, D // 2:] = 3.0, 3.0
+    k, v, q = (t.to(torch.bfloat16) for t in (k, v, q))
+    got, want, lim = attend_values(dev, k, v, q, 1, g)
+    assert (np.abs(got - want) <= lim).all()
+
+
+@pytest.mark.parametrize("D,g", ref.COMBOS)
+@pytest.mark.parametrize("late", [20, 50, 90])
+def test_a_later_key_of_small_values_takes_the_weight(dev, D, g, late):
+    """Large values at the first keys, then a key with nearly all the weight and
+    small values, in the same step or in a later one of the same warp."""
+    L = 100
+    k, v = torch.zeros(L, 1, D), randn((L, 1, D), 41).float()
+    k[late] = 4.0
+    v[:8] *= 2.0 ** 20
+    v[late] *= 2.0 ** -4
+    q = torch.full((1, 1, D), 96.0 / D ** 0.5 / 4)
+    k, v, q = (t.to(torch.bfloat16) for t in (k, v, q))
+    got, want, lim = attend_values(dev, k, v, q, 1, g)
+    assert (np.abs(got - want) <= lim).all()

@@ -559,8 +559,9 @@ __global__ void __launch_bounds__(kStoreThreads, kReadCtas<D>) kv4_read_kernel(c
 // weight and c = Z.)
 // The weights P_j S_j are rounded once to fp16 (2^-11 of each) for the second
 // product: w_j = 2^(s_j - m) S_j 2^-E, m a row's running maximum of s_j (in
-// powers of two) and E one exponent per warp that keeps the largest weight
-// near 1 whatever the sizes of V.  Both move only when a weight reaches 2^12
+// powers of two) and E an exponent per row that keeps the largest weight near 1
+// whatever the sizes of V (one for all rows of a warp would round a row by
+// values that only other rows see).  Both move only when a weight reaches 2^12
 // (fp16 holds those below 2^16).  The softmax's sum l of 2^(s_j - m) is fp32.
 //
 // Work.  Warps work alone: a warp takes a contiguous range of (head, block)
@@ -981,8 +982,8 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
             const int all_lo = p.window > 0 ? max(any_hi, 0) - p.window : 0;
 
             // ---- main loop ----
-            float acc[4 * VW][NB][4], l[NB][2], m[NB][2], vf = 1.0f;
-            int ve = kNoExp;                       // E; vf = 2^-E
+            float acc[4 * VW][NB][4], l[NB][2], m[NB][2], vf[NB][2];
+            int ve[NB][2];                         // E; vf = 2^-E
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -993,6 +994,8 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                 for (int c = 0; c < 2; ++c) {
                     l[nb][c] = 0.0f;
                     m[nb][c] = kNoMax;
+                    ve[nb][c] = kNoExp;
+                    vf[nb][c] = 1.0f;
                 }
             }
             for (int i = 0; i < steps; ++i) {
@@ -1138,21 +1141,21 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                                 float f = vs[rc][0][x];
 #pragma unroll
                                 for (int gr = 1; gr < NG; ++gr) f = fmaxf(f, vs[rc][gr][x]);
-                                f *= vf;
 #pragma unroll
                                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                                     for (int c = 0; c < 2; ++c) {
                                         const float q = ex2(s[rc][nb][2 * x + c] - m[nb][c]);
                                         lt[nb][c] += q;
-                                        raise |= q * f >= 4096.0f;
-                                        w[rc][nb][2 * x + c] = NG == 1 ? q * f : q * vf;
+                                        const float v = q * vf[nb][c], vS = v * f;
+                                        raise |= vS >= 4096.0f;
+                                        w[rc][nb][2 * x + c] = NG == 1 ? vS : v;
                                     }
                             }
                     };
                     weights();
                     if (__any_sync(0xFFFFFFFFu, raise)) {
-                        float fm[NB][2], top = 0.0f;
+                        float fm[NB][2];          // with the change of E
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -1163,8 +1166,11 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                                 for (int o = 4; o < 32; o <<= 1)
                                     d = fmaxf(d, __shfl_xor_sync(0xFFFFFFFFu, d, o));
                                 d = fmaxf(d, m[nb][c]);
-                                fm[nb][c] = ex2(m[nb][c] - d);
+                                const float moved = m[nb][c] - d;
+                                const float f = ex2(moved);
                                 m[nb][c] = d;
+                                l[nb][c] *= f;
+                                float top = 0.0f;               // the largest weight
 #pragma unroll
                                 for (int rc = 0; rc < 2; ++rc)
 #pragma unroll
@@ -1172,24 +1178,27 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
 #pragma unroll
                                         for (int gr = 0; gr < NG; ++gr)
                                             top = fmaxf(top, ex2(s[rc][nb][2 * x + c] - d) * vs[rc][gr][x]);
+#pragma unroll
+                                for (int o = 4; o < 32; o <<= 1)
+                                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+                                // E follows the weights so far down when m moves: a key
+                                // that no longer counts does not set the rounding
+                                const int old = ve[nb][c];
+                                const int e = min(max(old + (int)floorf(fmaxf(moved, -300.0f)),
+                                                      max((int)(__float_as_uint(top) >> 23) - 127, -100)), 100);
+                                ve[nb][c] = e;
+                                vf[nb][c] = __uint_as_float((uint32_t)(127 - e) << 23);
+                                fm[nb][c] = old == kNoExp ? 0.0f : ex2(moved + (float)(old - e));
                             }
-                        // the largest weight (all are >= 0: their bits order them)
-                        const uint32_t tb = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top));
-                        const int e = max(ve, min(max((int)(tb >> 23) - 127, -100), 100));
-                        const float fe = ve == kNoExp ? 1.0f : ex2((float)(ve - e));
-                        ve = e;
-                        vf = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                            for (int c = 0; c < 2; ++c) {
-                                l[nb][c] *= fm[nb][c];
+                            for (int c = 0; c < 2; ++c)
 #pragma unroll
                                 for (int z = 0; z < 4 * VW; ++z) {
-                                    acc[z][nb][c] *= fm[nb][c] * fe;
-                                    acc[z][nb][c + 2] *= fm[nb][c] * fe;
+                                    acc[z][nb][c] *= fm[nb][c];
+                                    acc[z][nb][c + 2] *= fm[nb][c];
                                 }
-                            }
                         weights();
                     }
 #pragma unroll
@@ -1269,7 +1278,6 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
             // ends inside it (the ring goes on to serve)
             const bool whole = u == item_begin && seg_end == item_end;
             const int which = whole || seg_end == w_end ? 1 : 0;
-            const float back = ve == kNoExp ? 0.0f : __uint_as_float((uint32_t)(127 + ve) << 23);   // 2^E
             float *slot = reinterpret_cast<float *>(
                 smem + (which ? L::ring_off + warp * L::ring : L::first_off + warp * L::slot));
 #pragma unroll
@@ -1278,6 +1286,9 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                 for (int c = 0; c < 2; ++c) {
                     const int row = 8 * nb + 2 * tig + c;
                     float t = l[nb][c];
+                    const float back = ve[nb][c] == kNoExp   // 2^E
+                                           ? 0.0f
+                                           : __uint_as_float((uint32_t)(127 + ve[nb][c]) << 23);
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
                     if (gid == 0) {
