@@ -602,7 +602,6 @@ struct AttnArgs {
 };
 
 constexpr float kNoMax = -1e30f;       // running maximum before any key
-constexpr int kNoExp = -1000;          // E before any key
 
 // A partial result of a row tile: [R][D + 4] fp32 sums, then m and l per row.
 template <int D, int NB>
@@ -982,8 +981,8 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
             const int all_lo = p.window > 0 ? max(any_hi, 0) - p.window : 0;
 
             // ---- main loop ----
-            float acc[4 * VW][NB][4], l[NB][2], m[NB][2], vf[NB][2];
-            int ve[NB][2];                         // E; vf = 2^-E
+            float acc[4 * VW][NB][4], l[NB][2], m[NB][2];
+            float vf[NB][2];                       // 2^-E
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -994,7 +993,6 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                 for (int c = 0; c < 2; ++c) {
                     l[nb][c] = 0.0f;
                     m[nb][c] = kNoMax;
-                    ve[nb][c] = kNoExp;
                     vf[nb][c] = 1.0f;
                 }
             }
@@ -1183,12 +1181,11 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                                     top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
                                 // E follows the weights so far down when m moves: a key
                                 // that no longer counts does not set the rounding
-                                const int old = ve[nb][c];
+                                const int old = 127 - (int)(__float_as_uint(vf[nb][c]) >> 23);
                                 const int e = min(max(old + (int)floorf(fmaxf(moved, -300.0f)),
                                                       max((int)(__float_as_uint(top) >> 23) - 127, -100)), 100);
-                                ve[nb][c] = e;
                                 vf[nb][c] = __uint_as_float((uint32_t)(127 - e) << 23);
-                                fm[nb][c] = old == kNoExp ? 0.0f : ex2(moved + (float)(old - e));
+                                fm[nb][c] = ex2(moved + (float)(old - e));
                             }
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb)
@@ -1286,9 +1283,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                 for (int c = 0; c < 2; ++c) {
                     const int row = 8 * nb + 2 * tig + c;
                     float t = l[nb][c];
-                    const float back = ve[nb][c] == kNoExp   // 2^E
-                                           ? 0.0f
-                                           : __uint_as_float((uint32_t)(127 + ve[nb][c]) << 23);
+                    const float back = 1.0f / vf[nb][c];     // 2^E, exact
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
                     if (gid == 0) {
