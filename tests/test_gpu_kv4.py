@@ -544,3 +544,21 @@ def test_a_later_key_of_small_values_takes_the_weight(dev, D, g, late):
     k, v, q = (t.to(torch.bfloat16) for t in (k, v, q))
     got, want, lim = attend_values(dev, k, v, q, 1, g)
     assert (np.abs(got - want) <= lim).all()
+
+
+def test_scores_far_below_zero(dev):
+    """Every score of a row near -1e35: the softmax is that of their differences
+    (one key in front by far), not that of a row without keys."""
+    H, D, g, L = 1, 128, 128, 20
+    k, v = torch.full((L, H, D), 1e17), randn((L, H, D), 51)
+    k[7] = 5e16
+    k = k.to(torch.bfloat16)
+    c = Cache(dev, [L], H, D, 16, g)
+    c.append(k.to(dev), v.to(dev), [L], [L])
+    q = torch.full((1, 2, D), -1e17, dtype=torch.bfloat16)
+    got = c.attend(q.to(dev), [L], [1]).cpu().double().numpy()
+    vq = ref.quantize(v, g)
+    want = ref.values(*vq, g)[7]
+    S = ref.bf16_f64(vq[1]).max()
+    # P is 1 at key 7 and 0 elsewhere: one weight S of 2^-11, and bf16's half step
+    assert (np.abs(got[0] - want) <= (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -18) * np.abs(want) + 2.0 ** -20 * S).all()

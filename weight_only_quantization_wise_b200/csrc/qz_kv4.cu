@@ -601,7 +601,7 @@ struct AttnArgs {
     unsigned int *err_word;
 };
 
-constexpr float kNoMax = -1e30f;       // running maximum before any key
+constexpr float kNoMax = -3.4e38f;     // running maximum before any key
 
 // A partial result of a row tile: [R][D + 4] fp32 sums, then m and l per row.
 template <int D, int NB>
