@@ -632,9 +632,8 @@ __device__ __forceinline__ void gemv_flush(float (&acc)[2][MB][4], const GemvArg
 // of B of a task (128 x rank, contiguous) come through the ring as further
 // stages behind the task's units: per adapter in use, 128, 64 or 32 rows at a
 // time, whatever fits a stage.
-// 16 tokens with adapters of their own, 28672 x 8192 int4, rank 64, warm: 66 us
-// with the first product; the plain GEMV alone takes 49, and 47 MB of B come on
-// top.  B read from global memory at the flush took 70 us, its stages in front of
+// 16 tokens with 11 adapters, 28672 x 8192 int4, rank 64, warm: 66 us with the
+// first product; the plain GEMV alone takes 49, and 40 MB of B come on top.  B read from global memory at the flush took 70 us, its stages in front of
 // the task's units 69 (67.5 then).  A kernel of its own for the second product
 // was as fast here (66), but one token, 4096 x 4096, rank 16, took 22 us cold
 // against 16 to 18.

@@ -15,8 +15,8 @@
 // h (times s_r) is kept as two bf16 values, h = hi + lo (2^-17 of h), the
 // operands of the second product.
 //
-// Bound by latency.  Alone, warm: 16 adapters of rank 64, K = 8192 (16.8 MB of
-// A) 8.9 us; 10 of rank 32, K = 4096 6.2 us; one of rank 16 4.1 us.  The GEMV is
+// Bound by latency.  Alone, warm: 11 adapters of rank 64, K = 8192 (11.5 MB of
+// A) 8.9 us; 9 of rank 32, K = 4096 6.2 us; one of rank 16 4.1 us.  The GEMV is
 // launched beside it and waits only before it uses h.
 #include <cuda_runtime.h>
 
