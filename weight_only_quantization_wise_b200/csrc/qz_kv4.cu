@@ -34,7 +34,10 @@ constexpr unsigned kErrIndex = 2u;     // bit of the device error word: bad page
 // of the 6449 GB/s of a copy); 35 thousand tokens read back cold 41 us (175 MB,
 // 0.66), 45 us without the next unit's record under way.  The read issues on
 // 0.37 of the cycles and waits mostly for loads (counters, before that
-// prefetch): latency, not instructions.  The append was not profiled.
+// prefetch): latency, not instructions.  The append issues on 0.45 with 12 warps
+// active per SM, and waits mostly for loads too; fetching the next unit's rows
+// to L2 or L1 first changed nothing (14.0 to 14.2 us), five CTAs per SM in place
+// of four took 16.0.
 struct StoreArgs {
     const uint16_t *k, *v;             // append: input
     uint16_t *k_out, *v_out;           // read: output
@@ -574,9 +577,10 @@ __global__ void __launch_bounds__(kStoreThreads, kReadCtas<D>) kv4_read_kernel(c
 //
 // Measured, 8 key heads of 128: 128 sequences of 1000..16000 tokens (785 MB, 32
 // query heads) 161 us warm, 176 cold: 0.69 of the copy bandwidth, at the power
-// limit (995 W, 1820 MHz).  A record of 16 tokens costs 271 warp instructions,
-// 113 of them integer and logic, 97 on the multiply pipes, 17 loads; they bind
-// before the bytes do.  Shorter calls are bound by launch, prologue and joins:
+// limit (995 W, 1820 MHz).  A record of 16 tokens costs 273 warp instructions,
+// 112 of them integer and logic, 99 on the multiply pipes, 17 loads and stores.
+// From 8 to 32 sequences the records stream at 0.78 of the copy bandwidth, and 19
+// us a call do not depend on the length (cold, by counters).  Shorter calls are bound by launch, prologue and joins:
 // one sequence of 131001 tokens (64 query heads, two scales per head, 147 MB) 51
 // us warm, one of 777 tokens 12 us.
 // Tried: three stages a ring instead of two (batch 167 against 170 us warm, 184
