@@ -93,6 +93,10 @@ enum {
     QZ_OP_W8A16_LORA_GEMV = 11
 };
 
+/* Bytes that let one split-K workspace serve calls of every size (see
+ * qz_workspace_bytes). */
+#define QZ_WORKSPACE_COUNTERS 8192
+
 /* FP4 formats (kind argument of the qz_fp4_* entry points). */
 enum {
     QZ_FP4_MX = 0,   /* MXFP4: blocks of 32, E8M0 (power-of-two) block scales */
@@ -120,10 +124,15 @@ QZ_API qz_status qz_packed_bytes(int64_t N, int64_t K, int32_t bits, int32_t sym
  * workspace of QZ_OP_QUANTIZE_PACK (per-tensor only) and of the GEMV/GEMM
  * paths that share tiles between CTAs must be zero-filled once before its
  * first use; every call that completes leaves its counters (and the
- * per-tensor word) at zero again, and the rest is scratch.  Where the counters
- * lie depends on op and sizes (and, for the decode GEMVs, on whether scales
- * and zeros are 16-byte aligned), so a buffer serves calls that agree in
- * those; between others it must be zero-filled again.  Host-only.  The kernels
+ * per-tensor word) at zero again, and the rest is scratch.
+ * The counters of the GEMVs and GEMMs (adapters and FP4 included) lie in the
+ * last QZ_WORKSPACE_COUNTERS bytes of a buffer that has that many more than a
+ * call needs.  So one buffer, passed whole, that is QZ_WORKSPACE_COUNTERS bytes
+ * larger than the largest of its calls needs serves all of them, whatever
+ * their sizes.  In a smaller one their place depends on op and sizes (and, for
+ * the decode GEMVs, on whether scales and zeros are 16-byte aligned): it serves
+ * calls that agree in those, and must be zero-filled again between others.
+ * Host-only.  The kernels
  * size their grids for the device's SM count (a B200 has 148; a device with
  * more is treated as 148); the size returned here serves every SM count up
  * to 148, so it does not depend on the device.

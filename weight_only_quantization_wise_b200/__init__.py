@@ -26,7 +26,7 @@ __all__ = [
     "qz_kv4_cache_bytes", "qz_kv4_append", "qz_kv4_read", "qz_kv4_attention",
     "QZ_OP_KV4_ATTENTION", "qz_w4a16_lora_gemv", "qz_w8a16_lora_gemv", "QZ_OP_W4A16_LORA_GEMV",
     "QZ_OP_W8A16_LORA_GEMV",
-    "Workspace", "QZ_OP_QUANTIZE_PACK", "QZ_OP_DEQUANTIZE", "QZ_OP_W4A16_GEMV",
+    "Workspace", "QZ_WORKSPACE_COUNTERS", "QZ_OP_QUANTIZE_PACK", "QZ_OP_DEQUANTIZE", "QZ_OP_W4A16_GEMV",
     "QZ_OP_W4A16_GEMM", "QZ_OP_W8A16_GEMV", "QZ_OP_W8A16_GEMM", "EXPORTED_SYMBOLS",
 ]
 
@@ -39,6 +39,7 @@ QZ_ERR_DEVICE_INDEX = 7
  QZ_OP_W8A16_GEMM, QZ_OP_GPTQ, QZ_OP_FP4A16_GEMV, QZ_OP_FP4A4_GEMM,
  QZ_OP_KV4_ATTENTION, QZ_OP_W4A16_LORA_GEMV, QZ_OP_W8A16_LORA_GEMV) = range(12)
 QZ_FP4_MX, QZ_FP4_NV = 0, 1
+QZ_WORKSPACE_COUNTERS = 8192
 FP4_BLOCK = {QZ_FP4_MX: 32, QZ_FP4_NV: 16}
 
 _i32, _i64, _sz, _p = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
@@ -169,50 +170,61 @@ def _handle(stream):
 
 
 class Workspace:
-    """Zero-filled device workspaces, one per kind and size of call.
+    """Device workspaces that grow on demand; one serves every call issued on
+    one stream.
 
-    Each call leaves the counters in its workspace at zero again (the rest is
-    scratch that every call writes before it reads).  Where the counters lie
-    depends on the call's sizes, and another call's scratch may cover them,
-    so calls of different sizes get different buffers: one Workspace serves
-    every call issued on one stream.  Calls that may run concurrently need
-    separate Workspace objects.
+    Each call leaves the counters in its workspace at zero again; the rest is
+    scratch that every call writes before it reads.  The split-K calls of every
+    size share one buffer, which is QZ_WORKSPACE_COUNTERS bytes larger than any
+    of them needs (their counters lie in its last bytes); `key` names the
+    zero-filled buffers of calls that keep their counters elsewhere.  A buffer
+    that a captured graph uses is kept when a larger one takes its place.
+    Calls that may run concurrently need separate Workspace objects.
     """
 
     def __init__(self, device=None):
         self.device = torch.device(device if device is not None else "cuda")
         self.bufs = {}
+        self.captured = {}              # address -> buffer a graph may use
 
     def get(self, nbytes: int, key=None):
+        """A zero-filled buffer: of the split-K calls, or of the calls `key` names."""
         if nbytes == 0:
             return None
-        key = nbytes if key is None else key
-        buf = self.bufs.get(key)
-        if buf is None or buf.numel() < nbytes:
-            buf = self.bufs[key] = torch.zeros(max(nbytes, 256), dtype=torch.uint8,
-                                               device=self.device)
-        return buf
+        return self._buffer(key, nbytes + QZ_WORKSPACE_COUNTERS if key is None else nbytes,
+                            torch.zeros)
 
     def get_scratch(self, nbytes: int):
-        """A second buffer for calls whose workspace is plain scratch (the
-        W4A4 GEMM's quantized activations): it is not zero-filled and must
-        not be the one the split-K calls count on."""
-        if getattr(self, "scratch", None) is None or self.scratch.numel() < nbytes:
-            self.scratch = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
-        return self.scratch
+        """A buffer for calls whose workspace is plain scratch (GPTQ, the W4A4
+        GEMM's quantized activations): not zero-filled, and not one that other
+        calls count on."""
+        return self._buffer("scratch", nbytes, torch.empty)
+
+    def _buffer(self, key, nbytes, make):
+        buf = self.bufs.get(key)
+        fits = buf is not None and buf.numel() >= nbytes
+        on_gpu = self.device.type == "cuda"
+        if on_gpu and torch.cuda.is_current_stream_capturing():
+            if not fits:                # filled, and kept, by the graph alone
+                return make(max(nbytes, 256), dtype=torch.uint8, device=self.device)
+            self.captured[buf.data_ptr()] = buf
+        elif not fits:
+            if on_gpu and buf is not None:      # calls of the current stream may still use it
+                buf.record_stream(torch.cuda.current_stream(self.device))
+            buf = self.bufs[key] = make(max(nbytes, 256), dtype=torch.uint8, device=self.device)
+        return buf
 
 
 def _ws_args(workspace, nbytes, device, key=None):
-    """Pointer and size of the call's workspace (`key`: what decides where its
-    counters lie, see Workspace).  Called inside
-    ``torch.cuda.stream(launch stream)``: a temporary workspace is then
-    allocated and zero-filled on the stream the kernel runs on, so the fill
-    is ordered before the kernel and the caching allocator hands the memory
-    out again only to work queued after it on that stream."""
+    """Pointer and size of the call's workspace (`key`: see Workspace.get).
+    Called inside ``torch.cuda.stream(launch stream)``: a temporary workspace
+    is then allocated and zero-filled on the stream the kernel runs on, so the
+    fill is ordered before the kernel and the caching allocator hands the
+    memory out again only to work queued after it on that stream."""
     if nbytes == 0:
         return None, 0
     if workspace is None:
-        workspace = Workspace(device).get(nbytes)
+        workspace = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
     elif isinstance(workspace, Workspace):
         workspace = workspace.get(nbytes, key)
     return _ptr(workspace), workspace.numel() * workspace.element_size()
@@ -238,7 +250,7 @@ def qz_quantize_pack(w, bits=4, symmetric=False, group_size=128, codes=None, sca
             shape = (1,) if group_size == 0 else (N, K // group_size)
             zeros = torch.empty(shape, dtype=torch.uint8, device=dev)
         ws_ptr, ws_bytes = _ws_args(workspace, qz_workspace_bytes(QZ_OP_QUANTIZE_PACK, 1, N, K,
-                                                                  group_size), dev)
+                                                                  group_size), dev, "quantize")
         _check(lib.qz_quantize_pack(_ptr(w), N, K, bits, int(symmetric), group_size,
                                     _ptr(codes), _ptr(scales),
                                     _ptr(zeros) if not symmetric else None, ws_ptr, ws_bytes,
@@ -268,13 +280,6 @@ def _matmul_out(a, N, y):
     return y
 
 
-def _matmul_key(op, M, N, K, g, scales, zeros):
-    """Workspace key of a split-K call: its sizes, and whether the scale and
-    zero arrays are aligned for the 256-wide plan."""
-    return (op, M, N, K, g, scales.data_ptr() % 16 == 0,
-            zeros is None or zeros.data_ptr() % 16 == 0)
-
-
 def qz_w4a16_gemv(a, codes, scales, zeros, N, K, group_size=128, y=None, workspace=None,
                   stream=None):
     """y = a * w_hat^T for int4 asymmetric group-wise weights, M <= 16."""
@@ -283,8 +288,7 @@ def qz_w4a16_gemv(a, codes, scales, zeros, N, K, group_size=128, y=None, workspa
     with _on(stream):
         y = _matmul_out(a, N, y)
         nbytes = qz_workspace_bytes(QZ_OP_W4A16_GEMV, M, N, K, group_size)
-        ws_ptr, ws_bytes = _ws_args(workspace, nbytes, a.device,
-                                    _matmul_key(QZ_OP_W4A16_GEMV, M, N, K, group_size, scales, zeros))
+        ws_ptr, ws_bytes = _ws_args(workspace, nbytes, a.device)
         _check(lib.qz_w4a16_gemv(_ptr(a), _ptr(codes), _ptr(scales), _ptr(zeros), M, N, K,
                                  group_size, _ptr(y), ws_ptr, ws_bytes, _handle(st)),
                "qz_w4a16_gemv")
@@ -299,8 +303,7 @@ def qz_w4a16_gemm(a, codes, scales, zeros, N, K, group_size=128, y=None, workspa
     with _on(stream):
         y = _matmul_out(a, N, y)
         nbytes = qz_workspace_bytes(QZ_OP_W4A16_GEMM, M, N, K, group_size)
-        ws_ptr, ws_bytes = _ws_args(workspace, nbytes, a.device,
-                                    _matmul_key(QZ_OP_W4A16_GEMM, M, N, K, group_size, scales, zeros))
+        ws_ptr, ws_bytes = _ws_args(workspace, nbytes, a.device)
         _check(lib.qz_w4a16_gemm(_ptr(a), _ptr(codes), _ptr(scales), _ptr(zeros), M, N, K,
                                  group_size, _ptr(y), ws_ptr, ws_bytes, _handle(st)),
                "qz_w4a16_gemm")
@@ -314,7 +317,7 @@ def qz_w8a16_gemv(a, codes, scales, N, K, y=None, workspace=None, stream=None):
     with _on(stream):
         y = _matmul_out(a, N, y)
         nbytes = qz_workspace_bytes(QZ_OP_W8A16_GEMV, M, N, K, K)
-        ws_ptr, ws_bytes = _ws_args(workspace, nbytes, a.device, (QZ_OP_W8A16_GEMV, M, N, K))
+        ws_ptr, ws_bytes = _ws_args(workspace, nbytes, a.device)
         _check(lib.qz_w8a16_gemv(_ptr(a), _ptr(codes), _ptr(scales), M, N, K, _ptr(y),
                                  ws_ptr, ws_bytes, _handle(st)), "qz_w8a16_gemv")
     return y
@@ -327,7 +330,7 @@ def qz_w8a16_gemm(a, codes, scales, N, K, y=None, workspace=None, stream=None):
     with _on(stream):
         y = _matmul_out(a, N, y)
         nbytes = qz_workspace_bytes(QZ_OP_W8A16_GEMM, M, N, K, K)
-        ws_ptr, ws_bytes = _ws_args(workspace, nbytes, a.device, (QZ_OP_W8A16_GEMM, M, N, K))
+        ws_ptr, ws_bytes = _ws_args(workspace, nbytes, a.device)
         _check(lib.qz_w8a16_gemm(_ptr(a), _ptr(codes), _ptr(scales), M, N, K, _ptr(y),
                                  ws_ptr, ws_bytes, _handle(st)), "qz_w8a16_gemm")
     return y
@@ -358,7 +361,7 @@ def qz_gptq_quantize(w, x, bits=4, symmetric=False, group_size=128, damp=0.01, c
         if workspace is None:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         elif isinstance(workspace, Workspace):
-            workspace = workspace.get(nbytes)
+            workspace = workspace.get_scratch(nbytes)
         _check(lib.qz_gptq_quantize(_ptr(w), _ptr(x), N, K, x.shape[0], bits, int(symmetric),
                                     group_size, float(damp), _ptr(codes), _ptr(scales),
                                     _ptr(zeros) if not symmetric else None, _ptr(workspace),
@@ -416,8 +419,7 @@ def qz_fp4a16_gemv(a, codes, scales, tensor_scale, N, K, kind, y=None, workspace
     with _on(stream):
         y = _matmul_out(a, N, y)
         nbytes = qz_workspace_bytes(QZ_OP_FP4A16_GEMV, M, N, K, 0)
-        ws_ptr, ws_bytes = _ws_args(workspace, nbytes, a.device,
-                                    _matmul_key(QZ_OP_FP4A16_GEMV, M, N, K, kind, scales, None))
+        ws_ptr, ws_bytes = _ws_args(workspace, nbytes, a.device)
         _check(lib.qz_fp4a16_gemv(_ptr(a), _ptr(codes), _ptr(scales), _ptr(tensor_scale), M, N,
                                   K, kind, _ptr(y), ws_ptr, ws_bytes, _handle(st)),
                "qz_fp4a16_gemv")
@@ -518,8 +520,7 @@ def qz_w4a16_lora_gemv(a, codes, scales, zeros, N, K, lora_a, lora_b, adapters, 
         cp = _array(codes, "codes", torch.uint8, N * K // 2, dev)
         sp = _array(scales, "scales", torch.bfloat16, N * (K // group_size), dev)
         zp = _array(zeros, "zeros", torch.uint8, N * (K // group_size), dev)
-        ws_ptr, ws_bytes = _ws_args(workspace, nbytes, dev, _matmul_key(
-            QZ_OP_W4A16_LORA_GEMV, M, N, K, group_size, scales, zeros))
+        ws_ptr, ws_bytes = _ws_args(workspace, nbytes, dev)
         _check(lib.qz_w4a16_lora_gemv(a.data_ptr(), cp, sp, zp, M, N, K, group_size, la, lb, ids, ls,
                                       n, rank, yp, ws_ptr, ws_bytes, _stream_of(dev, stream)),
                "qz_w4a16_lora_gemv")
@@ -539,7 +540,7 @@ def qz_w8a16_lora_gemv(a, codes, scales, N, K, lora_a, lora_b, adapters, lora_sc
         nbytes = qz_workspace_bytes(QZ_OP_W8A16_LORA_GEMV, M, N, K, K)
         cp = _array(codes, "codes", torch.uint8, N * K, dev)
         sp = _array(scales, "scales", torch.bfloat16, N, dev)
-        ws_ptr, ws_bytes = _ws_args(workspace, nbytes, dev, (QZ_OP_W8A16_LORA_GEMV, M, N, K))
+        ws_ptr, ws_bytes = _ws_args(workspace, nbytes, dev)
         _check(lib.qz_w8a16_lora_gemv(a.data_ptr(), cp, sp, M, N, K, la, lb, ids, ls, n, rank, yp,
                                       ws_ptr, ws_bytes, _stream_of(dev, stream)),
                "qz_w8a16_lora_gemv")

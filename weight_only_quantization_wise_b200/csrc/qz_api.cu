@@ -276,7 +276,8 @@ QZ_API qz_status qz_w4a16_gemv(const void *a, const void *codes, const void *sca
         gemv_plan(M, N, K, 4, device_sm_count(), gemv_unit_k(4, M, N, K, group_size, scales, zeros));
     s = check_workspace(plan.total_bytes, workspace, workspace_bytes);
     if (s != QZ_OK) return s;
-    return launch_w4a16_gemv(a, codes, scales, zeros, M, N, K, group_size, y, workspace, plan,
+    return launch_w4a16_gemv(a, codes, scales, zeros, M, N, K, group_size, y, workspace,
+                             split_counters(workspace, workspace_bytes, plan.partial_bytes), plan,
                              launch_overlap(), as_stream(stream));
 }
 
@@ -291,8 +292,9 @@ QZ_API qz_status qz_w8a16_gemv(const void *a, const void *codes, const void *sca
     const GemvPlan plan = gemv_plan(M, N, K, 8, device_sm_count());
     s = check_workspace(plan.total_bytes, workspace, workspace_bytes);
     if (s != QZ_OK) return s;
-    return launch_w8a16_gemv(a, codes, scales, M, N, K, y, workspace, plan, launch_overlap(),
-                             as_stream(stream));
+    return launch_w8a16_gemv(a, codes, scales, M, N, K, y, workspace,
+                             split_counters(workspace, workspace_bytes, plan.partial_bytes), plan,
+                             launch_overlap(), as_stream(stream));
 }
 
 QZ_API qz_status qz_w4a16_gemm(const void *a, const void *codes, const void *scales,
@@ -313,7 +315,7 @@ QZ_API qz_status qz_w4a16_gemm(const void *a, const void *codes, const void *sca
     const qz_status s = check_workspace(gemm_workspace_bytes(M, N, K), workspace, workspace_bytes);
     if (s != QZ_OK) return s;
     return launch_w4a16_gemm(a, codes, scales, zeros, M, N, K, group_size, y, workspace,
-                             as_stream(stream));
+                             workspace_bytes, as_stream(stream));
 }
 
 QZ_API qz_status qz_w8a16_gemm(const void *a, const void *codes, const void *scales,
@@ -329,7 +331,8 @@ QZ_API qz_status qz_w8a16_gemm(const void *a, const void *codes, const void *sca
         return QZ_ERR_ALIGNMENT;
     const qz_status s = check_workspace(gemm_workspace_bytes(M, N, K), workspace, workspace_bytes);
     if (s != QZ_OK) return s;
-    return launch_w8a16_gemm(a, codes, scales, M, N, K, y, workspace, as_stream(stream));
+    return launch_w8a16_gemm(a, codes, scales, M, N, K, y, workspace, workspace_bytes,
+                             as_stream(stream));
 }
 
 QZ_API qz_status qz_gptq_quantize(const void *w, const void *x, int64_t N, int64_t K,
@@ -419,7 +422,8 @@ QZ_API qz_status qz_fp4a16_gemv(const void *a, const void *codes, const void *bl
     s = check_workspace(plan.total_bytes, workspace, workspace_bytes);
     if (s != QZ_OK) return s;
     return launch_fp4a16_gemv(a, codes, block_scales, tensor_scale, M, N, K, kind, y, workspace,
-                              plan, launch_overlap(), as_stream(stream));
+                              split_counters(workspace, workspace_bytes, plan.partial_bytes), plan,
+                              launch_overlap(), as_stream(stream));
 }
 
 QZ_API void qz_set_device_wait_limit(uint64_t limit) {
@@ -496,7 +500,9 @@ qz_status lora_gemv(int bits, const void *a, const void *codes, const void *scal
     // The GEMV overlaps the kernel that makes h, which writes nothing else that
     // it reads and starts only after whatever was queued before this call.
     return launch_gemv_lora(bits, a, codes, scales, zeros, M, N, K, group_size, up, y,
-                            static_cast<char *>(workspace) + scratch, plan, st);
+                            static_cast<char *>(workspace) + scratch,
+                            split_counters(workspace, workspace_bytes, scratch + plan.partial_bytes),
+                            plan, st);
 }
 
 }  // namespace

@@ -903,7 +903,8 @@ int gemm_grid(const GemmSched &S, int sms, int ctas) {
 }
 
 // Workspace of a schedule: fp32 partial slots (sk_ctas + tail tiles - 1 of
-// act_rows x 128), then one uint32 arrival counter per tail tile.
+// act_rows x 128), then one uint32 arrival counter per tail tile (or the
+// buffer's last bytes, see split_counters: fewer than 2 * kSmCount tiles).
 size_t sched_partial_bytes(const GemmSched &S, int64_t M) {
     const int64_t slots = S.sk_ctas + (S.tiles - S.dp_tiles) - 1;
     return ((size_t)slots * slot_stride(gemm_act_rows(M)) * sizeof(float) + 255) & ~(size_t)255;
@@ -946,7 +947,7 @@ namespace {
 template <int BITS>
 qz_status launch_gemm(const void *a, const void *codes, const void *scales, const void *zeros,
                       int64_t M, int64_t N, int64_t K, int64_t group_size, void *y,
-                      void *workspace, cudaStream_t st) {
+                      void *workspace, size_t workspace_bytes, cudaStream_t st) {
     constexpr int kRowBytesPerK = BITS;   // code bytes of a row per 8 k
     const int act_rows = gemm_act_rows(M);
     const int ctas = gemm_ctas_per_sm(act_rows);
@@ -956,8 +957,7 @@ qz_status launch_gemm(const void *a, const void *codes, const void *scales, cons
     uint32_t *counters = nullptr;
     if (sched.sk_ctas > 0) {
         partials = static_cast<float *>(workspace);
-        counters = reinterpret_cast<uint32_t *>(static_cast<char *>(workspace) +
-                                                sched_partial_bytes(sched, M));
+        counters = split_counters(workspace, workspace_bytes, sched_partial_bytes(sched, M));
     }
     CUtensorMap act_map, pack_map, y_map;
     if (!make_map_2d(&act_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a, (uint64_t)K, (uint64_t)M,
@@ -1017,13 +1017,16 @@ qz_status launch_gemm(const void *a, const void *codes, const void *scales, cons
 
 qz_status launch_w4a16_gemm(const void *a, const void *codes, const void *scales,
                             const void *zeros, int64_t M, int64_t N, int64_t K,
-                            int64_t group_size, void *y, void *workspace, cudaStream_t st) {
-    return launch_gemm<4>(a, codes, scales, zeros, M, N, K, group_size, y, workspace, st);
+                            int64_t group_size, void *y, void *workspace, size_t workspace_bytes,
+                            cudaStream_t st) {
+    return launch_gemm<4>(a, codes, scales, zeros, M, N, K, group_size, y, workspace,
+                          workspace_bytes, st);
 }
 
 qz_status launch_w8a16_gemm(const void *a, const void *codes, const void *scales, int64_t M,
-                            int64_t N, int64_t K, void *y, void *workspace, cudaStream_t st) {
-    return launch_gemm<8>(a, codes, scales, nullptr, M, N, K, K, y, workspace, st);
+                            int64_t N, int64_t K, void *y, void *workspace, size_t workspace_bytes,
+                            cudaStream_t st) {
+    return launch_gemm<8>(a, codes, scales, nullptr, M, N, K, K, y, workspace, workspace_bytes, st);
 }
 
 }  // namespace qz

@@ -331,6 +331,7 @@ struct GemvArgs {
     int64_t units;             // tasks * kblocks
     int64_t ctas;              // launched CTAs (each owns at least one unit)
     int slots;
+    int count_by_task;         // a split task's counters: by the task, else by its first CTA
     int meta_span_shift;       // log2(units per meta slot) (kMetaTma)
     int fp4_bpu_shift;         // FP4: log2(scale blocks per 128-wide unit)
     int prefetch_early;        // launch overlap: weights may be read before the grid wait
@@ -615,8 +616,11 @@ __device__ __forceinline__ void gemv_flush(float (&acc)[2][MB][4], const GemvArg
             }
     __threadfence();
     __syncwarp();
+    // counters by the task or, when there are more tasks than CTAs, by the task's
+    // first CTA (no other split task begins there): at most ctas * 4 of them
+    uint32_t *counter = p.counters + (p.count_by_task ? (int64_t)task : first) * kConsumerWarps + w;
     uint32_t prev = 0;
-    if (lane == 0) prev = atomicAdd(&p.counters[sub], 1u);
+    if (lane == 0) prev = atomicAdd(counter, 1u);
     prev = __shfl_sync(0xFFFFFFFFu, prev, 0);
     if (prev != (uint32_t)(contributors - 1)) return;
     __threadfence();
@@ -624,7 +628,7 @@ __device__ __forceinline__ void gemv_flush(float (&acc)[2][MB][4], const GemvArg
     // for all tokens at once.
     reduce_slots<8 * MB, kRowsPerWarp>(base, slot_elems, contributors, p.M, lane, n0 + lane,
                                        p.N, p.y, out_scale);
-    if (lane == 0) p.counters[sub] = 0u;
+    if (lane == 0) *counter = 0u;
 }
 
 // ---- LORA: the adapters' part of a task's sums -----------------------------
@@ -1304,7 +1308,8 @@ bool two_half_ok(int64_t M, int64_t N, int64_t K, int64_t group_size, const void
 template <int BITS, bool LORA = false>
 qz_status launch_gemv(const void *a, const void *codes, const void *scales, const void *zeros,
                       int64_t M, int64_t N, int64_t K, int64_t group_size, void *y,
-                      void *workspace, const GemvPlan &plan, int overlap, cudaStream_t st,
+                      void *workspace, uint32_t *counters, const GemvPlan &plan, int overlap,
+                      cudaStream_t st,
                       const LoraUp *up = nullptr) {
     GemvArgs args;
     args.scales = static_cast<const uint16_t *>(scales);
@@ -1327,12 +1332,12 @@ qz_status launch_gemv(const void *a, const void *codes, const void *scales, cons
     args.counters = nullptr;
     if (plan.total_bytes > 0) {
         args.partials = static_cast<float *>(workspace);
-        args.counters =
-            reinterpret_cast<uint32_t *>(static_cast<char *>(workspace) + plan.partial_bytes);
+        args.counters = counters;
     }
     args.units = plan.tasks * plan.kblocks;
     args.ctas = plan.ctas;
     args.slots = (int)plan.slots;
+    args.count_by_task = plan.tasks <= plan.ctas;
     args.prefetch_early = LORA ? 0 : overlap;      // LORA waits for h alone
     args.wait_limit = device_wait_limit();
     args.err_word = device_error_word();
@@ -1398,8 +1403,8 @@ qz_status launch_gemv(const void *a, const void *codes, const void *scales, cons
 
 qz_status launch_fp4_gemv(const void *a, const void *codes, const void *scales,
                           const void *tensor_scale, int64_t M, int64_t N, int64_t K, int kind,
-                          void *y, void *workspace, const GemvPlan &plan, int overlap,
-                          cudaStream_t st) {
+                          void *y, void *workspace, uint32_t *counters, const GemvPlan &plan,
+                          int overlap, cudaStream_t st) {
     GemvArgs args{};
     args.fp4_scales = static_cast<const uint8_t *>(scales);
     args.tensor_scale = static_cast<const float *>(tensor_scale);
@@ -1416,12 +1421,12 @@ qz_status launch_fp4_gemv(const void *a, const void *codes, const void *scales,
     args.y = static_cast<uint16_t *>(y);
     if (plan.total_bytes > 0) {
         args.partials = static_cast<float *>(workspace);
-        args.counters =
-            reinterpret_cast<uint32_t *>(static_cast<char *>(workspace) + plan.partial_bytes);
+        args.counters = counters;
     }
     args.units = plan.tasks * plan.kblocks;
     args.ctas = plan.ctas;
     args.slots = (int)plan.slots;
+    args.count_by_task = plan.tasks <= plan.ctas;
     args.prefetch_early = overlap;
     args.wait_limit = device_wait_limit();
     args.err_word = device_error_word();
@@ -1474,6 +1479,8 @@ qz_status launch_fp4_gemv(const void *a, const void *codes, const void *scales,
 // layers from splitting every task over many CTAs).
 constexpr int64_t kMinUnitsPerCta = 4;
 
+static_assert(kSmCount * kMaxCtasPerSm * kConsumerWarps * sizeof(uint32_t) <= QZ_WORKSPACE_COUNTERS,
+              "the counters of every plan fit at a buffer's end");
 GemvPlan gemv_plan(int64_t M, int64_t N, int64_t K, int bits, int sms, int unit_k) {
     (void)bits;
     GemvPlan p{};
@@ -1539,36 +1546,37 @@ int gemv_unit_k(int bits, int64_t M, int64_t N, int64_t K, int64_t group_size,
 
 qz_status launch_w4a16_gemv(const void *a, const void *codes, const void *scales,
                             const void *zeros, int64_t M, int64_t N, int64_t K,
-                            int64_t group_size, void *y, void *workspace,
+                            int64_t group_size, void *y, void *workspace, uint32_t *counters,
                             const GemvPlan &plan, int overlap, cudaStream_t st) {
-    return launch_gemv<4>(a, codes, scales, zeros, M, N, K, group_size, y, workspace, plan,
-                          overlap, st);
+    return launch_gemv<4>(a, codes, scales, zeros, M, N, K, group_size, y, workspace, counters,
+                          plan, overlap, st);
 }
 
 qz_status launch_fp4a16_gemv(const void *a, const void *codes, const void *scales,
                              const void *tensor_scale, int64_t M, int64_t N, int64_t K, int kind,
-                             void *y, void *workspace, const GemvPlan &plan, int overlap,
-                             cudaStream_t st) {
-    return launch_fp4_gemv(a, codes, scales, tensor_scale, M, N, K, kind, y, workspace, plan,
+                             void *y, void *workspace, uint32_t *counters, const GemvPlan &plan,
+                             int overlap, cudaStream_t st) {
+    return launch_fp4_gemv(a, codes, scales, tensor_scale, M, N, K, kind, y, workspace, counters, plan,
                            overlap, st);
 }
 
 qz_status launch_w8a16_gemv(const void *a, const void *codes, const void *scales,
                             int64_t M, int64_t N, int64_t K, void *y, void *workspace,
-                            const GemvPlan &plan, int overlap, cudaStream_t st) {
-    return launch_gemv<8>(a, codes, scales, nullptr, M, N, K, K, y, workspace, plan, overlap,
+                            uint32_t *counters, const GemvPlan &plan, int overlap,
+                            cudaStream_t st) {
+    return launch_gemv<8>(a, codes, scales, nullptr, M, N, K, K, y, workspace, counters, plan, overlap,
                           st);
 }
 
 qz_status launch_gemv_lora(int bits, const void *a, const void *codes, const void *scales,
                            const void *zeros, int64_t M, int64_t N, int64_t K, int64_t group_size,
-                           const LoraUp &up, void *y, void *workspace, const GemvPlan &plan,
-                           cudaStream_t st) {
+                           const LoraUp &up, void *y, void *workspace, uint32_t *counters,
+                           const GemvPlan &plan, cudaStream_t st) {
     if (bits == 4)
         return launch_gemv<4, true>(a, codes, scales, zeros, M, N, K, group_size, y, workspace,
-                                    plan, 1, st, &up);
-    return launch_gemv<8, true>(a, codes, scales, nullptr, M, N, K, K, y, workspace, plan, 1, st,
-                                &up);
+                                    counters, plan, 1, st, &up);
+    return launch_gemv<8, true>(a, codes, scales, nullptr, M, N, K, K, y, workspace, counters, plan,
+                                1, st, &up);
 }
 
 }  // namespace qz

@@ -81,6 +81,8 @@ extern "C" QZ_API qz_status qz_w4a16_gemv_noalloc(const void *a, const void *cod
     }
     // plain stream order: the counter reset above is not a kernel, so a
     // programmatic dependency on it would not be ordered
-    return qz::launch_w4a16_gemv(a, codes, scales, zeros, M, N, K, group_size, y, scratch, plan,
-                                 0, static_cast<cudaStream_t>(stream));
+    return qz::launch_w4a16_gemv(a, codes, scales, zeros, M, N, K, group_size, y, scratch,
+                                 reinterpret_cast<uint32_t *>(static_cast<char *>(scratch) +
+                                                              plan.partial_bytes),
+                                 plan, 0, static_cast<cudaStream_t>(stream));
 }

@@ -91,6 +91,18 @@ qz_status launch_dequantize(const void *codes, const void *scales, const void *z
                             int64_t N, int64_t K, int bits, int symmetric,
                             int64_t group_size, void *w_hat, cudaStream_t stream);
 
+// Arrival counters of a split-K call whose partials take `partial_bytes` (a
+// multiple of 256): behind the partials; in a buffer that has
+// QZ_WORKSPACE_COUNTERS bytes to spare, in its last ones, a place that no
+// size of call moves and no partials reach.
+inline uint32_t *split_counters(void *workspace, size_t workspace_bytes, size_t partial_bytes) {
+    if (workspace == nullptr) return nullptr;
+    const size_t at = workspace_bytes >= partial_bytes + QZ_WORKSPACE_COUNTERS
+                          ? (workspace_bytes - QZ_WORKSPACE_COUNTERS) & ~(size_t)255
+                          : partial_bytes;
+    return reinterpret_cast<uint32_t *>(static_cast<char *>(workspace) + at);
+}
+
 // GEMV work plan (stream-K): the (128-row task x 128-wide K block) units
 // are split into equal contiguous ranges, one per launched CTA; each of a
 // CTA's four consumer warps owns 32 rows of every unit (a subtask), and a
@@ -106,7 +118,8 @@ struct GemvPlan {
     size_t counter_bytes; // uint32 arrival counter per 32-row subtask
     size_t total_bytes;
 };
-// Workspace: fp32 partials at offset 0, then one uint32 counter per subtask.
+// Workspace: fp32 partials at offset 0, then one uint32 counter per subtask
+// (where the counters lie in a larger buffer: split_counters).
 // `sms`: the SMs the grid is sized for (device_sm_count() at launch).
 GemvPlan gemv_plan(int64_t M, int64_t N, int64_t K, int bits, int sms, int unit_k = 128);
 // K per unit the int4 GEMV takes for these arguments (128 or 256); without
@@ -124,11 +137,12 @@ size_t gemv_workspace_bound(int64_t M, int64_t N, int64_t K, int bits, int max_u
 // `overlap`: qz_set_launch_overlap mode for this launch.
 qz_status launch_w4a16_gemv(const void *a, const void *codes, const void *scales,
                             const void *zeros, int64_t M, int64_t N, int64_t K,
-                            int64_t group_size, void *y, void *workspace,
+                            int64_t group_size, void *y, void *workspace, uint32_t *counters,
                             const GemvPlan &plan, int overlap, cudaStream_t stream);
 qz_status launch_w8a16_gemv(const void *a, const void *codes, const void *scales,
                             int64_t M, int64_t N, int64_t K, void *y, void *workspace,
-                            const GemvPlan &plan, int overlap, cudaStream_t stream);
+                            uint32_t *counters, const GemvPlan &plan, int overlap,
+                            cudaStream_t stream);
 
 // FP4 with block scales (qz_fp4.cu, qz_gemv.cu, qz_gemm_fp4.cu); kind 0 =
 // MXFP4, 1 = NVFP4.
@@ -139,8 +153,8 @@ qz_status launch_fp4_dequantize(const void *codes, const void *scales, const voi
                                 int64_t N, int64_t K, int kind, void *w_hat, cudaStream_t stream);
 qz_status launch_fp4a16_gemv(const void *a, const void *codes, const void *scales,
                              const void *tensor_scale, int64_t M, int64_t N, int64_t K, int kind,
-                             void *y, void *workspace, const GemvPlan &plan, int overlap,
-                             cudaStream_t stream);
+                             void *y, void *workspace, uint32_t *counters, const GemvPlan &plan,
+                             int overlap, cudaStream_t stream);
 
 // W4A4 GEMM: the MMA scale layout (atoms of 128 rows x 4 scales), the
 // in-call activation quantization and the block-scaled tcgen05 GEMM.
@@ -158,10 +172,11 @@ size_t gemm_workspace_bytes_for(int64_t M, int64_t N, int64_t K, int sms);
 size_t gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
 qz_status launch_w4a16_gemm(const void *a, const void *codes, const void *scales,
                             const void *zeros, int64_t M, int64_t N, int64_t K,
-                            int64_t group_size, void *y, void *workspace,
+                            int64_t group_size, void *y, void *workspace, size_t workspace_bytes,
                             cudaStream_t stream);
 qz_status launch_w8a16_gemm(const void *a, const void *codes, const void *scales, int64_t M,
-                            int64_t N, int64_t K, void *y, void *workspace, cudaStream_t stream);
+                            int64_t N, int64_t K, void *y, void *workspace,
+                            size_t workspace_bytes, cudaStream_t stream);
 
 // GPTQ (qz_gptq.cu): fp64 workspace of the damped Hessian factor, its
 // inverse, the working weights and one block of scaled errors.

@@ -23,8 +23,8 @@ qz_status launch_lora(const void *a, const void *lora_a, const void *lora_b, con
                       int64_t K, void *scratch, LoraUp *up, cudaStream_t stream);
 qz_status launch_gemv_lora(int bits, const void *a, const void *codes, const void *scales,
                            const void *zeros, int64_t M, int64_t N, int64_t K, int64_t group_size,
-                           const LoraUp &up, void *y, void *workspace, const GemvPlan &plan,
-                           cudaStream_t stream);
+                           const LoraUp &up, void *y, void *workspace, uint32_t *counters,
+                           const GemvPlan &plan, cudaStream_t stream);
 
 // The paged 4-bit key/value cache (qz_kv4.cu).
 struct Kv4Cache {
