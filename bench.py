@@ -259,7 +259,8 @@ class LayerSet:
         for N, K in LAYERS_70B:
             ws = max(ws, qz.qz_workspace_bytes(qz.QZ_OP_W4A16_GEMV, 1, N, K, GROUP),
                      qz.qz_workspace_bytes(qz.QZ_OP_W8A16_GEMV, 1, N, K, K))
-        self.ws = torch.zeros(ws, dtype=torch.uint8, device=dev)
+        # one buffer under calls of all these sizes
+        self.ws = torch.zeros(ws + qz.QZ_WORKSPACE_COUNTERS, dtype=torch.uint8, device=dev)
 
     # each part issues its launches for rotation p on the current stream
     def quant4(self, p):
@@ -542,8 +543,8 @@ def run_extras(qz, dev, pk, stream):
             a = synthetic.activations(Ms, K, seed=Ms, device=dev)
             y = torch.empty((Ms, N), dtype=torch.bfloat16, device=dev)
             ws = torch.zeros(max(256, qz.qz_workspace_bytes(qz.QZ_OP_W4A16_GEMM, Ms, N, K, GROUP),
-                                 qz.qz_workspace_bytes(qz.QZ_OP_W8A16_GEMM, Ms, N, K, K)),
-                             dtype=torch.uint8, device=dev)
+                                 qz.qz_workspace_bytes(qz.QZ_OP_W8A16_GEMM, Ms, N, K, K)) +
+                             qz.QZ_WORKSPACE_COUNTERS, dtype=torch.uint8, device=dev)
 
             def f4():
                 for c, s, z in packs4:
@@ -561,8 +562,8 @@ def run_extras(qz, dev, pk, stream):
                 # the same tokens through the decode GEMV (up to 64 tokens)
                 wsg = torch.zeros(max(256, qz.qz_workspace_bytes(qz.QZ_OP_W4A16_GEMV, Ms, N, K,
                                                                  GROUP),
-                                      qz.qz_workspace_bytes(qz.QZ_OP_W8A16_GEMV, Ms, N, K, K)),
-                                  dtype=torch.uint8, device=dev)
+                                      qz.qz_workspace_bytes(qz.QZ_OP_W8A16_GEMV, Ms, N, K, K)) +
+                                  qz.QZ_WORKSPACE_COUNTERS, dtype=torch.uint8, device=dev)
 
                 def g4():
                     for c, s, z in packs4:
