@@ -1,0 +1,81 @@
+"""Attention over the 4-bit cache where the values' sizes differ by far: groups of
+different sizes (needs a B200).  Every output channel is held to a bound of its
+own group's scales."""
+import numpy as np
+import pytest
+import torch
+
+import kv4_ref as ref
+import weight_only_quantization_wise_b200 as qz
+from test_gpu_kv4 import Cache, dev, randn  # noqa: F401  (dev is a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def expected(q, kq, vq, L, new, D, g, window=0, left_out=None):
+    """float64 result and bound of one sequence; left_out: (key, channel) pairs
+    that count with weight but without value (their channels are not compared).
+
+    Per channel, with the scales S of its own group (0 for a group of zeros,
+    which adds nothing): bf16's half step; 2^-11 of each weight P S, and 2^-25
+    of the largest for weights below fp16's normal range (2^-24 taken), times
+    |c - Z| <= 15; queries of 16 bits move a score by at most |scale| 2^-15 max|q|
+    sum|k| (and 2^-21 for its conversion), a P by the exponential of twice that;
+    ex2 and the fp32 sums 2^-20, a P below 2^-126 counts as 0; 16 keys per tensor
+    core sum, each off by at most 2^-22 of the largest magnitude, sum P S 15.
+    """
+    T, Hq, _ = q.shape
+    kf, vf = ref.values(*kq, g), ref.values(*vq, g)
+    codes, s, z = vq
+    S = ref.bf16_f64(s) * (codes.reshape(L, -1, D // g, g) != z[..., None]).any(-1)
+    S = np.repeat(S, g, -1)                                     # per channel
+    if left_out is not None:
+        S, vf = S.copy(), vf.copy()
+        S[left_out], vf[left_out] = 0.0, 0.0
+    H = kf.shape[1]
+    out, lim = np.zeros((T, Hq, D)), np.zeros((T, Hq, D))
+    scale = D ** -0.5
+    for i in range(new):
+        p = L - new + i
+        keep = np.arange(L) <= p
+        if window:
+            keep &= np.arange(L) > p - window
+        n = keep.sum()
+        if n == 0:
+            continue
+        for h in range(Hq):
+            kh, vh, Sh = (x[keep][:, h // (Hq // H)] for x in (kf, vf, S))
+            qh = q[i, h].double().numpy()
+            e = scale * (kh @ qh)
+            e = np.exp(e - e.max())
+            P = (e / e.sum())[:, None]
+            out[i, h] = (P * vh).sum(0)
+            pv = (P * np.abs(vh)).sum(0)
+            delta = scale * np.abs(qh).max() * np.abs(kh).sum(-1).max() * (2.0 ** -15 + 2.0 ** -21)
+            lim[i, h] = (2.0 ** -8 * np.abs(out[i, h]) +
+                         ((2.0 ** -11 + 2.0 ** -20) * pv +
+                          np.minimum(np.expm1(2 * delta) * pv, 2 * np.abs(vh).max(0))) * (1 + 2.0 ** -8) +
+                         (n / 16 + 8) * 2.0 ** -22 * 15 * (P * Sh).sum(0) +
+                         n * 15 * (2.0 ** -24 * (P * Sh).max(0) + 2.0 ** -126 * Sh.max(0)) + 2.0 ** -133)
+    return out, lim
+
+
+def check(dev, k, v, q, new, g, window=0):  # noqa: F811
+    L, H, D = k.shape
+    k, v, q = (x.to(torch.bfloat16) for x in (k, v, q))
+    c = Cache(dev, [L], H, D, 16, g)
+    c.append(k.to(dev), v.to(dev), [L], [L])
+    got = c.attend(q.to(dev), [L], [new], window=window).cpu().double().numpy()
+    want, lim = expected(q, ref.quantize(k, g), ref.quantize(v, g), L, new, D, g, window)
+    worst = (np.abs(got - want) / lim).max()
+    assert worst <= 1.0, worst                      # a NaN fails too
+    return got
+
+
+@pytest.mark.parametrize("D,g", [c for c in ref.COMBOS if c[0] > c[1]])
+@pytest.mark.parametrize("power", [-60, -40, -20, -12, 12, 20, 40, 60])
+def test_groups_of_different_sizes(dev, D, g, power):  # noqa: F811
+    L, new = 300, 2
+    k, v = randn((L, 1, D), 65, 0.3), randn((L, 1, D), 66).float()
+    v[..., :g] *= 2.0 ** power
+    check(dev, k, v, randn((new, 4, D), 67), new, g)

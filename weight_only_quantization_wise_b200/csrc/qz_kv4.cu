@@ -562,10 +562,12 @@ __global__ void __launch_bounds__(kStoreThreads, kReadCtas<D>) kv4_read_kernel(c
 // weight and c = Z.)
 // The weights P_j S_j are rounded once to fp16 (2^-11 of each) for the second
 // product: w_j = 2^(s_j - m) S_j 2^-E, m a row's running maximum of s_j (in
-// powers of two) and E an exponent per row that keeps the largest weight near 1
-// whatever the sizes of V (one for all rows of a warp would round a row by
-// values that only other rows see).  Both move only when a weight reaches 2^12
-// (fp16 holds those below 2^16).  The softmax's sum l of 2^(s_j - m) is fp32.
+// powers of two) and E an exponent per row and group of channels that keeps the
+// largest weight near 1 whatever the sizes of V (one for all rows of a warp would
+// round a row by values that only other rows see, one for all groups a group by
+// another's scales).  They move only when a weight reaches 2^12 (fp16 holds those
+// below 2^16) or the weights of a step 2^100.  The
+// softmax's sum l of 2^(s_j - m) is fp32.
 //
 // Work.  Warps work alone: a warp takes a contiguous range of (head, block)
 // units, keeps records of 16 tokens in a ring of its own (two per stage, one
@@ -655,6 +657,12 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// Larger of each half; a NaN is left out.
+__device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 __device__ __forceinline__ uint32_t f16x2_sub(uint32_t a, uint32_t b) {
@@ -986,7 +994,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
 
             // ---- main loop ----
             float acc[4 * VW][NB][4], l[NB][2], m[NB][2];
-            float vf[NB][2];                       // 2^-E
+            float vf[NG][NB][2];                   // 2^-E
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -997,7 +1005,8 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                 for (int c = 0; c < 2; ++c) {
                     l[nb][c] = 0.0f;
                     m[nb][c] = kNoMax;
-                    vf[nb][c] = 1.0f;
+#pragma unroll
+                    for (int gr = 0; gr < NG; ++gr) vf[gr][nb][c] = 0x1p126f;
                 }
             }
             for (int i = 0; i < steps; ++i) {
@@ -1129,35 +1138,44 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                                             s[rc][nb][2 * x + c] = __int_as_float(0x7FFFFFFF);
                             }
                     }
-                    // -- 2^(s - m) (times the scale when there is one per key): s is
-                    //    kept for the case that m moves
-                    float w[2][NB][4], lt[NB][2];
-                    bool raise = false;
+                    // -- weights 2^(s - m) S 2^-E in fp16, pairs of columns: s is kept
+                    //    for the case that m moves
+                    uint32_t w[2][NG][NB][2];
+                    float lt[NB][2];
+                    bool raise;
                     auto weights = [&]() {
+                        uint32_t top = 0u;                      // pair of the largest (NaN left out)
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb) lt[nb][0] = lt[nb][1] = 0.0f;
 #pragma unroll
                         for (int rc = 0; rc < 2; ++rc)
 #pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                float f = vs[rc][0][x];
+                            for (int x = 0; x < 2; ++x)
 #pragma unroll
-                                for (int gr = 1; gr < NG; ++gr) f = fmaxf(f, vs[rc][gr][x]);
+                                for (int nb = 0; nb < NB; ++nb) {
+                                    const float q0 = ex2(s[rc][nb][2 * x] - m[nb][0]);
+                                    const float q1 = ex2(s[rc][nb][2 * x + 1] - m[nb][1]);
+                                    lt[nb][0] += q0;
+                                    lt[nb][1] += q1;
 #pragma unroll
-                                for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                                    for (int c = 0; c < 2; ++c) {
-                                        const float q = ex2(s[rc][nb][2 * x + c] - m[nb][c]);
-                                        lt[nb][c] += q;
-                                        const float v = q * vf[nb][c], vS = v * f;
-                                        raise |= vS >= 4096.0f;
-                                        w[rc][nb][2 * x + c] = NG == 1 ? vS : v;
+                                    for (int gr = 0; gr < NG; ++gr) {
+                                        const float S = vs[rc][gr][x];
+                                        w[rc][gr][nb][x] = pack_f16x2(q0 * vf[gr][nb][0] * S,
+                                                                      q1 * vf[gr][nb][1] * S);
+                                        top = max_f16x2(top, w[rc][gr][nb][x]);
                                     }
-                            }
+                                }
+                        // 2^12 as fp16; l stays far from fp32's end
+                        raise = (top & 0xFFFFu) >= 0x6C00u || top >= 0x6C000000u;
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb)
+                            raise |= fmaxf(lt[nb][0], lt[nb][1]) >= 0x1p100f;
                     };
-                    weights();
-                    if (__any_sync(0xFFFFFFFFu, raise)) {
-                        float fm[NB][2];          // with the change of E
+                    // again when m and E have moved
+#pragma unroll 1
+                    for (bool moved = false;; moved = true) {
+                        weights();
+                        if (moved || !__any_sync(0xFFFFFFFFu, raise)) break;
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -1168,39 +1186,35 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                                 for (int o = 4; o < 32; o <<= 1)
                                     d = fmaxf(d, __shfl_xor_sync(0xFFFFFFFFu, d, o));
                                 d = fmaxf(d, m[nb][c]);
-                                const float moved = m[nb][c] - d;
-                                const float f = ex2(moved);
+                                const float down = m[nb][c] - d;
                                 m[nb][c] = d;
-                                l[nb][c] *= f;
-                                float top = 0.0f;               // the largest weight
+                                l[nb][c] *= ex2(down);
 #pragma unroll
-                                for (int rc = 0; rc < 2; ++rc)
+                                for (int gr = 0; gr < NG; ++gr) {
+                                    float top = 0.0f;           // the largest weight
 #pragma unroll
-                                    for (int x = 0; x < 2; ++x)
+                                    for (int rc = 0; rc < 2; ++rc)
 #pragma unroll
-                                        for (int gr = 0; gr < NG; ++gr)
+                                        for (int x = 0; x < 2; ++x)
                                             top = fmaxf(top, ex2(s[rc][nb][2 * x + c] - d) * vs[rc][gr][x]);
 #pragma unroll
-                                for (int o = 4; o < 32; o <<= 1)
-                                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-                                // E follows the weights so far down when m moves: a key
-                                // that no longer counts does not set the rounding
-                                const int old = 127 - (int)(__float_as_uint(vf[nb][c]) >> 23);
-                                const int e = min(max(old + (int)floorf(fmaxf(moved, -300.0f)),
-                                                      max((int)(__float_as_uint(top) >> 23) - 127, -100)), 100);
-                                vf[nb][c] = __uint_as_float((uint32_t)(127 - e) << 23);
-                                fm[nb][c] = ex2(moved + (float)(old - e));
-                            }
+                                    for (int o = 4; o < 32; o <<= 1)
+                                        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+                                    // E follows the weights so far down when m moves: a key
+                                    // that no longer counts does not set the rounding
+                                    const int old = 127 - (int)(__float_as_uint(vf[gr][nb][c]) >> 23);
+                                    int e = (int)(__float_as_uint(top) >> 23) - 127;
+                                    e = max(e, old + (int)floorf(fmaxf(down, -300.0f)));
+                                    e = min(max(e, -126), 100);
+                                    const float f = ex2(down + (float)(old - e));
 #pragma unroll
-                        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                                for (int z = 0; z < 4 * VW; ++z) {
-                                    acc[z][nb][c] *= fm[nb][c];
-                                    acc[z][nb][c + 2] *= fm[nb][c];
+                                    for (int z = gr * G / 16; z < (gr + 1) * G / 16; ++z) {
+                                        acc[z][nb][c] *= f;
+                                        acc[z][nb][c + 2] *= f;
+                                    }
+                                    vf[gr][nb][c] = __uint_as_float((uint32_t)(127 - e) << 23);
                                 }
-                        weights();
+                            }
                     }
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb) {
@@ -1217,11 +1231,8 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
 #pragma unroll
                             for (int x = 0; x < 2; ++x)
 #pragma unroll
-                                for (int gr = 0; gr < NG; ++gr) {
-                                    const float f = NG == 1 ? 1.0f : vs[rc][gr][x];
-                                    wf[gr][nb][x] = transpose8(
-                                        pack_f16x2(w[rc][nb][2 * x] * f, w[rc][nb][2 * x + 1] * f));
-                                }
+                                for (int gr = 0; gr < NG; ++gr)
+                                    wf[gr][nb][x] = transpose8(w[rc][gr][nb][x]);
                         uint32_t vw[2][KW];
 #pragma unroll
                         for (int q = 0; q < (2 * KW + 3) / 4; ++q) {
@@ -1287,7 +1298,10 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                 for (int c = 0; c < 2; ++c) {
                     const int row = 8 * nb + 2 * tig + c;
                     float t = l[nb][c];
-                    const float back = 1.0f / vf[nb][c];     // 2^E, exact
+                    float back[NG];                          // 2^E
+#pragma unroll
+                    for (int gr = 0; gr < NG; ++gr)
+                        back[gr] = __uint_as_float((254u << 23) - __float_as_uint(vf[gr][nb][c]));
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
                     if (gid == 0) {
@@ -1301,7 +1315,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
 #pragma unroll
                             for (int hi = 0; hi < 2; ++hi)
                                 slot[row * SL::pitch + 64 * wi + 16 * nib + 8 * hi + gid] =
-                                    acc[4 * wi + nib][nb][2 * hi + c] * back;
+                                    acc[4 * wi + nib][nb][2 * hi + c] * back[(64 * wi + 16 * nib) / G];
                 }
             if (whole) {
                 __syncwarp();
@@ -1473,8 +1487,8 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
 // ---------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------
-// CTAs per SM, and warps per CTA so that the accumulators and queries of NB
-// 8-row tiles stay in registers (and the rings of 4 groups in shared memory).
+// CTAs per SM, and warps per CTA so that the accumulators, the queries and what
+// each group of channels needs stay in registers, but for a few words.
 // D = 128, warm: one CTA of 16 warps against two of 8, half the parts to join:
 // one long sequence 51, 58 us, batch 166, 171.  D = 64 has many short items and
 // takes two: 17 sequences of draft tokens 27 us, with one CTA 32.
@@ -1483,7 +1497,7 @@ template <int D, int NB>
 constexpr int kAttnCtas = D == 128 && NB == 1 ? 1 : kAttnCtasPerSm;
 template <int D, int G, int NB>
 constexpr int kAttnWarps =
-    D == 256 ? 4 : NB == 2 ? 6 : D == 64 ? 8 : G == 32 ? 14 : 16;
+    D == 256 ? 4 : NB == 2 ? (D == 128 ? 4 : 6) : D == 64 ? 8 : G == 128 ? 16 : 12;
 
 // Rows of a tile: 8 or 16.  A tile of 16 reads and unpacks the keys once for
 // twice the rows, but has half the warps per CTA and twice the products and
