@@ -492,7 +492,8 @@ QZ_API qz_status qz_kv4_read(const void *cache, const void *page_table, const vo
  * q_heads % kv_heads == 0; scale finite; window >= 0 (0: none).
  * fp32 softmax and sums; queries enter as 16-bit fixed-point numbers relative
  * to their row's largest value, the weights P_j S_j as fp16 relative to the
- * largest so far of the row and the group of channels.  A row with an infinity or a NaN in q gives NaN.  Values of
+ * largest so far of the row and the group of channels (groups of zeros left
+ * out).  A row with an infinity or a NaN in q gives NaN.  Values of
  * magnitude above 2^96 in the cache may overflow.  Results do not depend on
  * timing (they depend on the device's SM count through the split of the work).
  * Workspace: qz_workspace_bytes(QZ_OP_KV4_ATTENTION, 1, 1, head_dim, 0)

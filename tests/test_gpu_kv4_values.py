@@ -1,6 +1,7 @@
-"""Attention over the 4-bit cache where the values' sizes differ by far: groups of
-different sizes (needs a B200).  Every output channel is held to a bound of its
-own group's scales."""
+"""Attention over the 4-bit cache where the values' sizes differ by far: keys whose
+values are all zero, groups of a head that are all zero, groups of different
+sizes (needs a B200).  Every output channel is held to a bound of its own group's
+scales."""
 import numpy as np
 import pytest
 import torch
@@ -72,6 +73,41 @@ def check(dev, k, v, q, new, g, window=0):  # noqa: F811
     return got
 
 
+def led_keys(L, D, at, lead, seed):
+    """Keys of small scores, but for one that leads by about `lead` powers of two
+    under a query of ones."""
+    k = randn((L, 1, D), seed, 0.3).float()
+    k[at] = lead * 0.6931 / D ** 0.5
+    return k
+
+
+@pytest.mark.parametrize("D,g", ref.COMBOS)
+@pytest.mark.parametrize("at", [0, 17, 200, 399])
+@pytest.mark.parametrize("std,lead", [(0.02, 14), (1e-3, 8), (1e-3, 14), (1e-5, 4), (1e-6, 0),
+                                      (1e-30, 6)])
+def test_a_key_of_zeros_beside_small_values(dev, D, g, at, std, lead):  # noqa: F811
+    """A key whose value is zero (its scale is stored as 1) holds most of the
+    weight; the others' small values still count in full."""
+    L = 400
+    v = randn((L, 1, D), 61).float() * std
+    v[at] = 0.0
+    check(dev, led_keys(L, D, at, lead, 60), v, torch.ones(1, 2, D), 1, g)
+
+
+@pytest.mark.parametrize("D,g", [c for c in ref.COMBOS if c[0] > c[1]])
+@pytest.mark.parametrize("std", [1.0, 1e-3, 1e-6])
+@pytest.mark.parametrize("alive_from", [10 ** 6, 250, 385, 398])
+def test_a_group_of_zeros(dev, D, g, std, alive_from):  # noqa: F811
+    """The last group of a padded head is zero in every key, or up to a late one:
+    the live groups, and the late values, count in full."""
+    L, new = 400, 4
+    k, v = randn((L, 1, D), 62, 0.3), randn((L, 1, D), 63).float() * std
+    v[:alive_from, :, -g:] = 0.0
+    got = check(dev, k, v, randn((new, 2, D), 64), new, g)
+    if alive_from > L:
+        assert (got[..., -g:] == 0.0).all()
+
+
 @pytest.mark.parametrize("D,g", [c for c in ref.COMBOS if c[0] > c[1]])
 @pytest.mark.parametrize("power", [-60, -40, -20, -12, 12, 20, 40, 60])
 def test_groups_of_different_sizes(dev, D, g, power):  # noqa: F811
@@ -79,3 +115,18 @@ def test_groups_of_different_sizes(dev, D, g, power):  # noqa: F811
     k, v = randn((L, 1, D), 65, 0.3), randn((L, 1, D), 66).float()
     v[..., :g] *= 2.0 ** power
     check(dev, k, v, randn((new, 4, D), 67), new, g)
+
+
+@pytest.mark.parametrize("D,g", ref.COMBOS)
+@pytest.mark.parametrize("L,new,share,window", [(9000, 1, 8, 0), (700, 70, 8, 0), (700, 70, 8, 40),
+                                                (48, 48, 2, 0)])
+def test_zeros_among_many_rows_and_parts(dev, D, g, L, new, share, window):  # noqa: F811
+    """Keys of zeros at the front and scattered, zero groups, small values, over
+    parts of CTAs, 16-row tiles, windows and rows that see zeros alone."""
+    H = 2
+    k, v = randn((L, H, D), 68, 0.3).float(), randn((L, H, D), 69).float() * 1e-4
+    gen = torch.Generator().manual_seed(70)
+    v *= (torch.rand(L, H, D // g, 1, generator=gen) < 0.7).expand(L, H, D // g, g).reshape(L, H, D)
+    v[:33] = 0.0
+    k[:2] += 0.5
+    check(dev, k, v, torch.ones(new, H * share, D) + randn((new, H * share, D), 71, 0.2), new, g, window)

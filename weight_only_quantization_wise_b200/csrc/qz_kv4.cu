@@ -566,7 +566,8 @@ __global__ void __launch_bounds__(kStoreThreads, kReadCtas<D>) kv4_read_kernel(c
 // largest weight near 1 whatever the sizes of V (one for all rows of a warp would
 // round a row by values that only other rows see, one for all groups a group by
 // another's scales).  They move only when a weight reaches 2^12 (fp16 holds those
-// below 2^16) or the weights of a step 2^100.  The
+// below 2^16) or the weights of a step 2^100.  A group of zeros, which is stored
+// with S = 1, adds nothing and sets no E: it is looked for when E would move.  The
 // softmax's sum l of 2^(s_j - m) is fp32.
 //
 // Work.  Warps work alone: a warp takes a contiguous range of (head, block)
@@ -755,6 +756,50 @@ __device__ __forceinline__ void store4(uint16_t *dst, float4 o, float f) {
         dst[0] = (uint16_t)a; dst[1] = (uint16_t)(a >> 16);
         dst[2] = (uint16_t)b; dst[3] = (uint16_t)(b >> 16);
     }
+}
+
+// Which groups of the lane's tokens (gid, gid + 8 of two records) hold zeros
+// alone, as bits 4 group + 2 record + half.  Such a group has S = 1, Z = 0.
+template <int D, int G>
+__device__ __noinline__ uint32_t zero_groups(const uint8_t *r0, const uint8_t *r1, int lane) {
+    constexpr int NG = D / G;
+    const int gid = lane >> 2, tig = lane & 3;
+    uint32_t zeros = 0u, ones = 0u;                // ones: S = 1
+#pragma unroll
+    for (int gr = 0; gr < NG; ++gr)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (*reinterpret_cast<const uint16_t *>((i >> 1 ? r1 : r0) + v_scales_off(D, NG) + 32 * gr +
+                                                    2 * (gid + 8 * (i & 1))) == 0x3F80u)
+                ones |= 1u << (4 * gr + i);
+    const uint32_t some = __reduce_or_sync(0xFFFFFFFFu, ones);
+#pragma unroll 1
+    for (int gr = 0; gr < NG; ++gr) {
+        if (!(some >> (4 * gr) & 15u)) continue;
+        uint32_t bits[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint8_t *rec = i >> 1 ? r1 : r0;
+            const int t = gid + 8 * (i & 1);
+            bits[i] = rec[v_zeros_off(D, NG) + 16 * gr + t];
+#pragma unroll
+            for (int w = 0; w < (G < 64 ? 1 : G / 64); ++w)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {      // units 4 tig + u of a 64-wide span's 16
+                    const uint32_t unit = *reinterpret_cast<const uint16_t *>(
+                        rec + v_codes_off(D) +
+                        v_unit_byte(D, t, gr * G / 64 + w, tig >> 1, 4 * (tig & 1) + u));
+                    bits[i] |= G >= 64 ? unit : unit & (gr & 1 ? 0xFF00u : 0x00FFu);
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            bits[i] |= __shfl_xor_sync(0xFFFFFFFFu, bits[i], 1);
+            bits[i] |= __shfl_xor_sync(0xFFFFFFFFu, bits[i], 2);
+            if (bits[i] == 0u) zeros |= 1u << (4 * gr + i);
+        }
+    }
+    return zeros & ones;
 }
 
 // What a row's sums are multiplied with at the end: 1 / l; 0 for a row that
@@ -1171,11 +1216,36 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                         for (int nb = 0; nb < NB; ++nb)
                             raise |= fmaxf(lt[nb][0], lt[nb][1]) >= 0x1p100f;
                     };
-                    // again when m and E have moved
+                    // a second pass when groups of zeros have left, a last one when m and
+                    // E have moved
 #pragma unroll 1
-                    for (bool moved = false;; moved = true) {
+                    for (int pass = 0;;) {
                         weights();
-                        if (moved || !__any_sync(0xFFFFFFFFu, raise)) break;
+                        if (pass == 2 || !__any_sync(0xFFFFFFFFu, raise)) break;
+                        if (pass == 0) {
+                            // a group of zeros is stored with S = 1, Z = 0 and adds nothing:
+                            // it sets no E
+                            bool one = false;
+#pragma unroll
+                            for (int rc = 0; rc < 2; ++rc)
+#pragma unroll
+                                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                                    for (int gr = 0; gr < NG; ++gr) one |= vs[rc][gr][x] == 1.0f;
+                            if (__any_sync(0xFFFFFFFFu, one)) {
+                                const uint32_t zeros = zero_groups<D, G>(sr[0], sr[1], lane);
+#pragma unroll
+                                for (int rc = 0; rc < 2; ++rc)
+#pragma unroll
+                                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                                        for (int gr = 0; gr < NG; ++gr)
+                                            if (zeros >> (4 * gr + 2 * rc + x) & 1u) vs[rc][gr][x] = 0.0f;
+                                pass = 1;
+                                continue;
+                            }
+                        }
+                        pass = 2;
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
