@@ -493,7 +493,9 @@ QZ_API qz_status qz_kv4_read(const void *cache, const void *page_table, const vo
  * fp32 softmax and sums; queries enter as 16-bit fixed-point numbers relative
  * to their row's largest value, the weights P_j S_j as fp16 relative to the
  * largest so far of the row and the group of channels (groups of zeros left
- * out).  A row with an infinity or a NaN in q gives NaN.  Values of
+ * out).  A row with an infinity or a NaN in q gives NaN; an
+ * infinite value leaves the channels of its group not finite in the rows that
+ * see its key, and changes no others.  Values of
  * magnitude above 2^96 in the cache may overflow.  Results do not depend on
  * timing (they depend on the device's SM count through the split of the work).
  * Workspace: qz_workspace_bytes(QZ_OP_KV4_ATTENTION, 1, 1, head_dim, 0)

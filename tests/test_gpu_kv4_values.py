@@ -1,7 +1,7 @@
 """Attention over the 4-bit cache where the values' sizes differ by far: keys whose
 values are all zero, groups of a head that are all zero, groups of different
-sizes (needs a B200).  Every output channel is held to a bound of its own group's
-scales."""
+sizes, values that are not finite (needs a B200).  Every output channel is held
+to a bound of its own group's scales."""
 import numpy as np
 import pytest
 import torch
@@ -130,3 +130,28 @@ def test_zeros_among_many_rows_and_parts(dev, D, g, L, new, share, window):  # n
     v[:33] = 0.0
     k[:2] += 0.5
     check(dev, k, v, torch.ones(new, H * share, D) + randn((new, H * share, D), 71, 0.2), new, g, window)
+
+
+@pytest.mark.parametrize("D,g", ref.COMBOS)
+@pytest.mark.parametrize("L,at,new", [(400, 150, 1), (400, 398, 1), (400, 399, 3), (400, 0, 2)])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf")])
+def test_an_infinite_value_stays_in_its_group(dev, D, g, L, at, new, value):  # noqa: F811
+    """The channels of the group that holds it are not finite in the rows that see
+    the key, whatever step of the sequence it stands in; all others are right."""
+    k, v = randn((L, 1, D), 72, 0.3), randn((L, 1, D), 73)
+    fine = v.clone()
+    v[at, 0, 5] = value
+    c = Cache(dev, [L], 1, D, 16, g)
+    c.append(k.to(dev), v.to(dev), [L], [L])
+    q = randn((new, 2, D), 74)
+    got = c.attend(q.to(dev), [L], [new]).cpu().double().numpy()
+    left_out = np.zeros((L, 1, D), bool)
+    left_out[at, 0, :g] = True                       # the group's other values at that key too
+    want, lim = expected(q, ref.quantize(k, g), ref.quantize(fine, g), L, new, D, g, 0, left_out)
+    for i in range(new):
+        sees = at <= L - new + i
+        good = slice(g if sees else 0, None)
+        if sees:
+            assert not np.isfinite(got[i, :, :g]).any()
+        assert (np.abs(got[i, :, good] - want[i, :, good]) <= lim[i, :, good]).all(), i
+    assert qz.qz_device_status() == 0

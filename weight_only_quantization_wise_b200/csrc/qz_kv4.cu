@@ -1148,6 +1148,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                             for (int rc = 0; rc < 2; ++rc)      // existing keys without a page
                                 if (!((got >> rc) & 1u) && 2 * i + rc < nblk && key0 + 16 * rc < sw.len)
                                     atomicOr(p.err_word, kErrIndex);
+                        bool wild = false;
                         // keys each column's row may see: [klo, khi)
                         int khi[NB][2], klo[NB][2];
 #pragma unroll
@@ -1163,25 +1164,50 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                             for (int x = 0; x < 2; ++x) {
                                 const int key = key0 + 16 * rc + gid + 8 * x;
                                 const bool none = !((got >> rc) & 1u) || key >= sw.len;
-                                // a scale that is not finite (values that were not) makes
-                                // the rows that see the key NaN, and may not reach the
-                                // others through 0 * inf
-                                bool wild = false;
-#pragma unroll
-                                for (int gr = 0; gr < NG; ++gr) wild |= !(vs[rc][gr][x] <= 3.4e38f);
-                                if (none || wild) {             // none: not written, whatever it holds
+                                if (none) {                     // not written, whatever it holds
 #pragma unroll
                                     for (int gr = 0; gr < NG; ++gr) vs[rc][gr][x] = 0.0f;
                                 }
+#pragma unroll
+                                for (int gr = 0; gr < NG; ++gr) wild |= !(vs[rc][gr][x] <= 3.4e38f);
 #pragma unroll
                                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                                     for (int c = 0; c < 2; ++c)
                                         if (none || key >= khi[nb][c] || key < klo[nb][c])
                                             s[rc][nb][2 * x + c] = __int_as_float(0xFF800000);
-                                        else if (wild)
-                                            s[rc][nb][2 * x + c] = __int_as_float(0x7FFFFFFF);
                             }
+                        // a scale that is not finite (values that were not) makes its group
+                        // NaN in the rows that see the key, as it does in a step that all see,
+                        // and may not reach the others through 0 * inf
+                        if (__any_sync(0xFFFFFFFFu, wild)) {
+                            uint32_t spoilt = 0u;              // groups of columns
+#pragma unroll
+                            for (int rc = 0; rc < 2; ++rc)
+#pragma unroll
+                                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                                    for (int gr = 0; gr < NG; ++gr)
+                                        if (!(vs[rc][gr][x] <= 3.4e38f)) {
+                                            vs[rc][gr][x] = 0.0f;
+#pragma unroll
+                                            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                                                for (int c = 0; c < 2; ++c)
+                                                    if (s[rc][nb][2 * x + c] != __int_as_float(0xFF800000))
+                                                        spoilt |= 1u << (NG * (2 * nb + c) + gr);
+                                        }
+#pragma unroll
+                            for (int o = 4; o < 32; o <<= 1) spoilt |= __shfl_xor_sync(0xFFFFFFFFu, spoilt, o);
+#pragma unroll
+                            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                                    for (int z = 0; z < 4 * VW; ++z)
+                                        if (spoilt >> (NG * (2 * nb + c) + 16 * z / G) & 1u)
+                                            acc[z][nb][c] = acc[z][nb][c + 2] = __int_as_float(0x7FFFFFFF);
+                        }
                     }
                     // -- weights 2^(s - m) S 2^-E in fp16, pairs of columns: s is kept
                     //    for the case that m moves
