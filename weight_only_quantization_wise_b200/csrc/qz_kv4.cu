@@ -63,6 +63,7 @@ struct StoreLayout {
     static constexpr int rec = (int)record_bytes(D, G);
     static constexpr int tile = 32 * kChunkPitch;           // the values of a pass
     static constexpr int per_warp = tile + rec;
+    static_assert(rec >= 2 * D, "append_token's buffer");
     static_assert(kReadCtas<D> * (kStoreWarps * per_warp + 4096) <= 228 * 1024, "the CTAs fit on an SM");
 };
 
@@ -168,6 +169,14 @@ __device__ __noinline__ uint32_t codes8_exact(uint4 x, float s, float z) {
     return word;
 }
 
+// One value as codes8 (or, where the inverse overflows, codes8_exact) forms it,
+// values that are not finite included.
+__device__ __forceinline__ uint32_t code4(float x, float s, float inv, float z) {
+    if (!(inv < __int_as_float(0x7F800000))) return code4_exact(x, s, z);
+    const float y = __fadd_rn(__fmaf_rn(x, inv, __fadd_rn(z, 192.0f)), 12582912.0f - 192.0f);
+    return min(__float_as_uint(y), 0x4B40000Fu) & 0x0Fu;
+}
+
 // Transposes 4 x 8 nibbles: words a, b, c, d of 8 nibbles -> units g = 0..7 of
 // four nibbles (a_g, b_g, c_g, d_g); out[0] = units 0, 2, out[1] = 4, 6,
 // out[2] = 1, 3, out[3] = 5, 7 (low half, high half).
@@ -212,12 +221,12 @@ __device__ __forceinline__ uint32_t group_scale(float lo, float hi, float &s, fl
     if (s == 0.0f) s = 1.0f;
     const uint32_t sb = dev::bf16_round_up_bits(s);
     s = __uint_as_float(sb << 16);
-    z = -rintf(__fdiv_rn(lo, s));
+    z = (float)(int)-rintf(__fdiv_rn(lo, s));      // 0 for a NaN
     return sb;
 }
 
 // One token of one head into its record `dst`; a lane holds D / 32 consecutive
-// values of the keys, then of the values.  `buf`: D bytes of the warp's own.
+// values of the keys, then of the values.  `buf`: 2 D bytes of the warp's own.
 template <int D, int G>
 __device__ __forceinline__ void append_token(const uint16_t *k, const uint16_t *v, int t, uint8_t *dst,
                                              uint8_t *buf, int lane) {
@@ -251,11 +260,12 @@ __device__ __forceinline__ void append_token(const uint16_t *k, const uint16_t *
         }
         float s, z;
         const uint32_t sb = group_scale(mn, mx, s, z);
+        const float inv = __frcp_rn(s);
 #pragma unroll
         for (int i = 0; i < V / 2; ++i) {
-            buf[which * D + lane * V + 2 * i] = (uint8_t)code4_exact(dev::bf16_lo(w[which][i]), s, z);
+            buf[which * D + lane * V + 2 * i] = (uint8_t)code4(dev::bf16_lo(w[which][i]), s, inv, z);
             buf[which * D + lane * V + 2 * i + 1] =
-                (uint8_t)code4_exact(dev::bf16_hi(w[which][i]), s, z);
+                (uint8_t)code4(dev::bf16_hi(w[which][i]), s, inv, z);
         }
         if ((lane & (LPG - 1)) == 0) {
             const int so = 16 * (lane / LPG) + t;
