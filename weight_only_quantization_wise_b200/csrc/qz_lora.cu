@@ -21,6 +21,7 @@
 #include <cuda_runtime.h>
 
 #include "qz_lora.cuh"
+#include "qz_lora_index.cuh"
 #include "qz_serving.cuh"
 
 namespace qz {
@@ -91,7 +92,8 @@ lora_down_kernel(const LoraArgs p) {
     const bool v0 = j0 + gid < p.R, v1 = j0 + gid + 8 < p.R;
     const int steps = p.K / 32;                              // K is a multiple of 128
     const int w = rank * kDownWarps + warp;
-    const int s0 = w * steps / (kCluster * kDownWarps), s1 = (w + 1) * steps / (kCluster * kDownWarps);
+    const int s0 = lora::part_begin(w, steps, kCluster * kDownWarps);
+    const int s1 = lora::part_begin(w + 1, steps, kCluster * kDownWarps);
     const uint4 none = make_uint4(0u, 0u, 0u, 0u);
     while (mask) {
         const bool two = __popcll(mask) > 8;
