@@ -1042,7 +1042,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                 }
             }
             // keys that all rows, and that any row, of the tile may see
-            const int pos0 = sw.len - sw.n;
+            const int pos0 = sw.pos0;
             const int r0 = rt * R, r1 = min(r0 + R, sw.n * p.share) - 1;
             const int all_hi = pos0 + r0 / p.share + 1, any_hi = pos0 + r1 / p.share + 1;
             const int all_lo = p.window > 0 ? max(any_hi, 0) - p.window : 0;

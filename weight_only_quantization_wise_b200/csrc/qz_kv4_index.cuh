@@ -118,7 +118,8 @@ QZ_HD int block_hi(const StoreWork &s, int block) {
 // the sequence's rows may see.  Every item has at least one unit, so that
 // rows without keys are written too.
 struct SeqWork {
-    int n, len;           // queries, keys
+    int n, len;           // queries, keys (none behind the page table's end)
+    int pos0;             // position of the first query
     int block0;           // first block of keys
     int blocks;           // units of an item (>= 1)
     int row_tiles;        // row tiles per key head
@@ -132,9 +133,12 @@ QZ_HD SeqWork seq_work(int cu0, int cu1, int kv_len, int rows, int capacity, int
     s.n = cu0 >= 0 && cu1 > cu0 ? cu1 - cu0 : 0;
     if (s.n > rows) s.n = rows;
     s.len = kv_len < 0 ? 0 : (kv_len > capacity ? capacity : kv_len);
-    const int64_t first = window > 0 ? (int64_t)s.len - s.n - window + 1 : 0;
-    s.block0 = first > 0 ? (int)(first / kBlock) : 0;
+    // (capacity, the multiple of 16 that len ends at, cuts no record)
+    s.pos0 = (kv_len < 0 ? 0 : kv_len) - s.n;
+    const int64_t first = window > 0 ? (int64_t)s.pos0 - window + 1 : 0;
     const int end = (int)(((int64_t)s.len + kBlock - 1) / kBlock);
+    s.block0 = first > 0 ? (int)(first / kBlock) : 0;
+    if (s.block0 >= end) s.block0 = end > 0 ? end - 1 : 0;
     s.blocks = end - s.block0 > 1 ? end - s.block0 : 1;
     s.row_tiles = (int)(((int64_t)s.n * share + tile_rows - 1) / tile_rows);
     s.units = (int64_t)s.row_tiles * kv_heads * s.blocks;
