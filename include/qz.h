@@ -391,7 +391,9 @@ QZ_API qz_status qz_fp4a4_gemm(const void *a, const void *codes, const void *sca
  *               none, and the next qz_device_status reports QZ_ERR_DEVICE_INDEX
  *   lora_scales fp32 [n_adapters]
  * rank: a multiple of 8, at most 128 (adapters of lower rank are padded with
- * zeros).  Only adapters in use are read, each once.  Other arguments,
+ * zeros).  Only adapters in use are read, each once.  The call's GEMV overlaps
+ * its own first kernel, whatever qz_set_launch_overlap says, and nothing in
+ * front of the call.  Other arguments,
  * requirements and errors as for the plain GEMVs.  Workspace:
  * qz_workspace_bytes(QZ_OP_W4A16_LORA_GEMV, M, N, K, group_size) or
  * (QZ_OP_W8A16_LORA_GEMV, M, N, K, K) bytes, zero-filled before first use.
