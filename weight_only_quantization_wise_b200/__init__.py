@@ -186,33 +186,43 @@ class Workspace:
         self.device = torch.device(device if device is not None else "cuda")
         self.bufs = {}
         self.captured = {}              # address -> buffer a graph may use
+        self.on_cuda = self.device.type == "cuda"
+        self._capturing = (torch._C._cuda_isCurrentStreamCapturing if self.on_cuda
+                           else lambda: False)
 
     def get(self, nbytes: int, key=None):
         """A zero-filled buffer: of the split-K calls, or of the calls `key` names."""
         if nbytes == 0:
             return None
-        return self._buffer(key, nbytes + QZ_WORKSPACE_COUNTERS if key is None else nbytes,
-                            torch.zeros)
+        if key is None:
+            nbytes += QZ_WORKSPACE_COUNTERS
+        buf = self.bufs.get(key)
+        if buf is None or buf.numel() < nbytes or self._capturing():
+            return self._other(key, nbytes, torch.zeros)
+        return buf
 
     def get_scratch(self, nbytes: int):
         """A buffer for calls whose workspace is plain scratch (GPTQ, the W4A4
         GEMM's quantized activations): not zero-filled, and not one that other
         calls count on."""
-        return self._buffer("scratch", nbytes, torch.empty)
+        buf = self.bufs.get("scratch")
+        if buf is None or buf.numel() < nbytes or self._capturing():
+            return self._other("scratch", nbytes, torch.empty)
+        return buf
 
-    def _buffer(self, key, nbytes, make):
+    def _other(self, key, nbytes, make):
+        """The buffer of a call in a capture, or of one that needs a larger one."""
         buf = self.bufs.get(key)
         fits = buf is not None and buf.numel() >= nbytes
-        on_gpu = self.device.type == "cuda"
-        if on_gpu and torch.cuda.is_current_stream_capturing():
+        if self._capturing():
             if not fits:                # filled, and kept, by the graph alone
                 return make(max(nbytes, 256), dtype=torch.uint8, device=self.device)
             self.captured[buf.data_ptr()] = buf
-        elif not fits:
-            if on_gpu and buf is not None:      # calls of the current stream may still use it
-                buf.record_stream(torch.cuda.current_stream(self.device))
-            buf = self.bufs[key] = make(max(nbytes, 256), dtype=torch.uint8, device=self.device)
-        return buf
+            return buf
+        if buf is not None and self.on_cuda:    # calls of the current stream may still use it
+            buf.record_stream(torch.cuda.current_stream(self.device))
+        self.bufs[key] = make(max(nbytes, 256), dtype=torch.uint8, device=self.device)
+        return self.bufs[key]
 
 
 def _ws_args(workspace, nbytes, device, key=None):
@@ -226,7 +236,10 @@ def _ws_args(workspace, nbytes, device, key=None):
     if workspace is None:
         workspace = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
     elif isinstance(workspace, Workspace):
-        workspace = workspace.get(nbytes, key)
+        buf = workspace.get(nbytes, key)
+        if not workspace.on_cuda:
+            raise ValueError("the workspace must live on a CUDA device")
+        return buf.data_ptr(), buf.numel()
     return _ptr(workspace), workspace.numel() * workspace.element_size()
 
 
