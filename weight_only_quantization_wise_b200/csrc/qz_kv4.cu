@@ -1042,7 +1042,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                 }
             }
             // keys that all rows, and that any row, of the tile may see
-            const int pos0 = sw.pos0;
+            const int pos0 = first_position(p.kv_lens[b], sw.n);
             const int r0 = rt * R, r1 = min(r0 + R, sw.n * p.share) - 1;
             const int all_hi = pos0 + r0 / p.share + 1, any_hi = pos0 + r1 / p.share + 1;
             const int all_lo = p.window > 0 ? max(any_hi, 0) - p.window : 0;
@@ -1254,11 +1254,13 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                     };
                     // a second pass when groups of zeros have left, a last one when m and
                     // E have moved
+                    bool moved = false, cleared = false;
 #pragma unroll 1
-                    for (int pass = 0;;) {
+                    for (;;) {
                         weights();
-                        if (pass == 2 || !__any_sync(0xFFFFFFFFu, raise)) break;
-                        if (pass == 0) {
+                        if (!__any_sync(0xFFFFFFFFu, raise) || moved) break;
+                        if (!cleared) {
+                            cleared = true;
                             // a group of zeros is stored with S = 1, Z = 0 and adds nothing:
                             // it sets no E
                             bool one = false;
@@ -1277,11 +1279,10 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
 #pragma unroll
                                         for (int gr = 0; gr < NG; ++gr)
                                             if (zeros >> (4 * gr + 2 * rc + x) & 1u) vs[rc][gr][x] = 0.0f;
-                                pass = 1;
                                 continue;
                             }
                         }
-                        pass = 2;
+                        moved = true;
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -1603,7 +1604,7 @@ template <int D, int NB>
 constexpr int kAttnCtas = D == 128 && NB == 1 ? 1 : kAttnCtasPerSm;
 template <int D, int G, int NB>
 constexpr int kAttnWarps =
-    D == 256 ? 4 : NB == 2 ? (D == 128 ? 4 : 6) : D == 64 ? 8 : G == 128 ? 16 : 12;
+    D == 256 ? 4 : NB == 2 ? (D == 128 ? 4 : 6) : D == 64 ? 8 : 12;
 
 // Rows of a tile: 8 or 16.  A tile of 16 reads and unpacks the keys once for
 // twice the rows, but has half the warps per CTA and twice the products and

@@ -119,12 +119,15 @@ QZ_HD int block_hi(const StoreWork &s, int block) {
 // rows without keys are written too.
 struct SeqWork {
     int n, len;           // queries, keys (none behind the page table's end)
-    int pos0;             // position of the first query
     int block0;           // first block of keys
     int blocks;           // units of an item (>= 1)
     int row_tiles;        // row tiles per key head
     int64_t units;        // kv_heads * row_tiles * blocks (0 when n == 0)
 };
+
+// Position of the first of a sequence's n queries (len may end before them: at
+// the page table's end).
+QZ_HD int first_position(int kv_len, int n) { return (kv_len < 0 ? 0 : kv_len) - n; }
 
 // rows: the call's token rows (rows * share < 2^31); capacity < 2^31 - 16.
 QZ_HD SeqWork seq_work(int cu0, int cu1, int kv_len, int rows, int capacity, int window, int share,
@@ -134,8 +137,7 @@ QZ_HD SeqWork seq_work(int cu0, int cu1, int kv_len, int rows, int capacity, int
     if (s.n > rows) s.n = rows;
     s.len = kv_len < 0 ? 0 : (kv_len > capacity ? capacity : kv_len);
     // (capacity, the multiple of 16 that len ends at, cuts no record)
-    s.pos0 = (kv_len < 0 ? 0 : kv_len) - s.n;
-    const int64_t first = window > 0 ? (int64_t)s.pos0 - window + 1 : 0;
+    const int64_t first = window > 0 ? (int64_t)first_position(kv_len, s.n) - window + 1 : 0;
     const int end = (int)(((int64_t)s.len + kBlock - 1) / kBlock);
     s.block0 = first > 0 ? (int)(first / kBlock) : 0;
     if (s.block0 >= end) s.block0 = end > 0 ? end - 1 : 0;
