@@ -118,6 +118,22 @@ def test_groups_of_different_sizes(dev, D, g, power):  # noqa: F811
 
 
 @pytest.mark.parametrize("D,g", ref.COMBOS)
+@pytest.mark.parametrize("rise", [0.0, 0.02, 0.3, 3.0])
+@pytest.mark.parametrize("alive", [None, 37, 180, 399])
+def test_zeros_alone_while_scores_rise(dev, D, g, rise, alive):  # noqa: F811
+    """Every value zero, or all but one key's: scores that rise by `rise` powers of
+    two a key move the maximum far while no exponent has been set."""
+    L = 400
+    v = torch.zeros(L, 1, D)
+    if alive is not None:
+        v[alive] = randn((1, D), 75) * 1e-3
+    k = (torch.arange(L).float() * rise * 0.6931 / D ** 0.5)[:, None, None].expand(L, 1, D)
+    got = check(dev, k, v, torch.ones(1, 2, D), 1, g)
+    if alive is None:
+        assert (got == 0.0).all()
+
+
+@pytest.mark.parametrize("D,g", ref.COMBOS)
 @pytest.mark.parametrize("L,new,share,window", [(9000, 1, 8, 0), (700, 70, 8, 0), (700, 70, 8, 40),
                                                 (48, 48, 2, 0)])
 def test_zeros_among_many_rows_and_parts(dev, D, g, L, new, share, window):  # noqa: F811

@@ -1240,9 +1240,9 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
                                     lt[nb][1] += q1;
 #pragma unroll
                                     for (int gr = 0; gr < NG; ++gr) {
-                                        const float S = vs[rc][gr][x];
-                                        w[rc][gr][nb][x] = pack_f16x2(q0 * vf[gr][nb][0] * S,
-                                                                      q1 * vf[gr][nb][1] * S);
+                                        const float S = vs[rc][gr][x];   // first: 0 keeps q 2^-E finite
+                                        w[rc][gr][nb][x] = pack_f16x2(q0 * S * vf[gr][nb][0],
+                                                                      q1 * S * vf[gr][nb][1]);
                                         top = max_f16x2(top, w[rc][gr][nb][x]);
                                     }
                                 }
