@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(kStoreThreads, kReadCtas<D>) kv4_read_kernel(c
 // m16n8k32 with exact 32-bit sums.  Z and S stay out of the product:
 //   sum_d q_d S (c - Z) = S 2^-e (sum_d i_d c - Z sum_d i_d).
 // (As fp16 products with c - Z formed per code, the scores took 9 instructions
-// for 8 codes; the kernel is bound by its instructions.)
+// for 8 codes.)
 // For the values the codes enter the tensor cores as the exact fp16 integers
 // c - Z.  Of a 16-bit half, nibble 0 ORed under fp16 1024 is 1024 + c and
 // nibble 1 under 64 is 64 + c (one LOP3 each for the same nibble of both
@@ -589,18 +589,17 @@ __global__ void __launch_bounds__(kStoreThreads, kReadCtas<D>) kv4_read_kernel(c
 // the workspace by the last to arrive, parts added in order.
 //
 // Measured, 8 key heads of 128: 128 sequences of 1000..16000 tokens (785 MB, 32
-// query heads) 161 us warm, 176 cold: 0.69 of the copy bandwidth, at the power
-// limit (995 W, 1820 MHz).  A record of 16 tokens costs 273 warp instructions,
-// 112 of them integer and logic, 99 on the multiply pipes, 17 loads and stores.
-// From 8 to 32 sequences the records stream at 0.78 of the copy bandwidth, and 19
-// us a call do not depend on the length (cold, by counters).  Shorter calls are bound by launch, prologue and joins:
-// one sequence of 131001 tokens (64 query heads, two scales per head, 147 MB) 51
-// us warm, one of 777 tokens 12 us.
-// Tried: three stages a ring instead of two (batch 167 against 170 us warm, 184
-// against 180 cold: not a matter of latency); two CTAs of 6 warps instead of 8
-// (201, 200); fp16 products for the scores (197 us cold against 180).  Without
-// the subtraction of Z from the codes of V (a timing probe) the batch took 11%
-// less, but the subnormal codes that would allow it lose low bits in the product.
+// query heads) 165 us warm, 180 cold: 0.68 of the copy bandwidth; one sequence of
+// 131001 tokens (64 query heads, two scales per head, 147 MB) 49 us warm, one of 777
+// tokens 11 us.  A record of 16 tokens costs 262 warp instructions, 108 of them
+// integer and logic, 94 on the multiply pipes, 16 loads and stores, 16 tensor
+// products.  At 32 sequences the schedulers issue on 0.53 of the cycles, the ALU pipe
+// is busy for 0.43 and the tensor pipe for 0.23 of them, and the three warps of a
+// scheduler wait mostly for the results of earlier instructions: latency of
+// dependent instructions, no unit that is full.  From 8 to 32 sequences the records
+// stream at 0.81 of the copy bandwidth, and 20 us a call do not depend on the length.
+// Keys whose group is all zeros cost a search each step while nothing else has been
+// seen (64 x 4000 tokens, the last of four groups zero: 93 us, 134).
 struct AttnArgs {
     const uint16_t *q;
     int64_t q_stride;                  // elements between tokens
@@ -1596,9 +1595,13 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attention_kernel(const A
 // ---------------------------------------------------------------------------
 // CTAs per SM, and warps per CTA so that the accumulators, the queries and what
 // each group of channels needs stay in registers, but for a few words.
-// D = 128, warm: one CTA of 16 warps against two of 8, half the parts to join:
-// one long sequence 51, 58 us, batch 166, 171.  D = 64 has many short items and
-// takes two: 17 sequences of draft tokens 27 us, with one CTA 32.
+// D = 128, warm: one CTA of 12 warps against two of 6, half the parts to join:
+// one sequence of 131001 tokens 49, 59 us, 128 sequences 165, 173.  D = 64 has many
+// short items and takes two: 17 sequences of draft tokens 28.5 us, with one CTA of 16
+// warps 29.8.  64 x 4000 tokens, 8 key heads of 128, 4 query heads each, warm: groups
+// of 32 94 us with 12 warps, 121 with 14 of 128 registers; of 64 76, 81 with 16; of
+// 128 68, 71 with 16.  16-row tiles of groups of 32 (16 query heads): 137 with 4
+// warps, 190 with 6.
 constexpr int kAttnCtasPerSm = 2;      // at most
 template <int D, int NB>
 constexpr int kAttnCtas = D == 128 && NB == 1 ? 1 : kAttnCtasPerSm;
@@ -1608,16 +1611,20 @@ constexpr int kAttnWarps =
 
 // Rows of a tile: 8 or 16.  A tile of 16 reads and unpacks the keys once for
 // twice the rows, but has half the warps per CTA and twice the products and
-// softmax per step.  Warm, 8 key heads, 8- against 16-row tiles:
-//   D = 64, one scale per head:   64 x 4000 tokens, 16 rows per key head 84, 68 us;
-//       512 rows 2165, 1606; 1 x 32000, 16 rows 23, 31; 128 rows 81, 67
-//   D = 128, g = 32:   64 x 4000, 16 rows 187, 175; 512 rows 5315, 4526
-//   D = 128, g = 64:   16 rows 134, 146; 512 rows 3590, 3740
-//   D = 128, g = 128:  16 rows 116, 124; 512 rows 3321, 3105; 1 x 32000, 16 rows 30, 46
-//   D = 256, g = 128:  16 rows 196, 250; 128 rows 1550, 1856
-// So 16 for 64-wide heads and for groups of 32, when a sequence has more than 8
-// rows on average and the 8-row tiles come to 128 or more (below that the longer
-// tiles leave the machine idle).
+// softmax per step.  Warm, 8 key heads, 8- against 16-row tiles, us:
+//                     64 x 4000 tokens,       1 x 32000 tokens,
+//                     16 rows   512 rows      16 rows   128 rows  per key head
+//   D = 64,  g = 32   104  87   2667  2096    27  35     99   85
+//   D = 64,  g = 64    88  71   2293  1695    24  33     85   70
+//   D = 128, g = 32   166 137   4701  3593    38  48    163  134
+//   D = 128, g = 64   132 109   3949  2816    35  43    133  107
+//   D = 128, g = 128  119  98   3538  2530    32  40    118   97
+//   D = 256, g = 64   241 366   7941 10746     -         227  356
+//   D = 256, g = 128  199 277   6855  7967     -         238  269
+// 16 when a sequence has more than 8 rows on average and the 8-row tiles come to
+// 128 or more (below that the longer tiles leave the machine idle), for 64-wide
+// heads and for groups of 32.  The rule is older than the four warps of 128-wide
+// tiles, with which groups of 64 and 128 would gain as well.
 template <int D, int G>
 constexpr bool kTallTiles = D == 64 || G == 32;
 bool tall_tiles(const AttnArgs &p) {
@@ -1645,12 +1652,13 @@ qz_status launch_attn(const AttnArgs &in, cudaStream_t st) {
         }) != cudaSuccess)
         return QZ_ERR_CUDA;
     // two steps of two blocks per warp at least, as a CTA's prologue and join
-    // outweigh a shorter loop.  Mixed batch of 12, D = 256, 16-row tiles, warm: 2,
-    // 4, 8 units per warp 35, 35, 42 us; other calls alike.
+    // outweigh a shorter loop.  Eight sequences of 100..3000 tokens, 32 query and 8 key
+    // heads of 128, warm: 2, 4, 8 units per warp 20.6, 20.6, 21.4 us; one of 32000 or
+    // 131001, 64 of 4000, drafts with a window and a mixed batch alike.
     AttnArgs args = in;
     args.min_units = 4 * W;
     // items alike of up to six steps per warp whole in a CTA, not cut: one
-    // sequence of 777 tokens 11.7 us, cut 18.5; other calls alike
+    // sequence of 777 tokens 10.8 us, cut 17.5; the calls above alike
     args.whole_units = 12 * W;
     kernel<<<(unsigned)(device_sm_count() * C), 32 * W, L::bytes, st>>>(args);
     return launch_status();
